@@ -20,8 +20,9 @@ HEADER_PATH = os.path.join(HERE, "..", "include", "bsq.h")
 BSQ_BF16, BSQ_FP8_E4M3_B128, BSQ_MXFP4, BSQ_NVFP4, BSQ_FP8_E4M3_TENSOR, BSQ_FP8_E5M2_TENSOR = 0, 1, 2, 3, 4, 5
 BSQ_OK, BSQ_ERR_INVALID_ARG, BSQ_ERR_UNSUPPORTED, BSQ_ERR_CUDA, BSQ_ERR_TIMEOUT = 0, 1, 2, 3, 4
 BSQ_NEEDS_GRAD_X, BSQ_NEEDS_GRAD_W = 1, 2
+BSQ_DT_BF16, BSQ_DT_F32 = 0, 1
 
-_c_void_p, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_c_void_p, _i64, _i32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double
 
 SIGNATURES = {
     "bsq_dequant": [_i32, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p],
@@ -41,6 +42,14 @@ SIGNATURES = {
     "bsq_linear_backward_e5m2": [_c_void_p, _i64, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p,
                                  _c_void_p, _c_void_p, _i64, ctypes.c_uint32, _i32, _c_void_p, _c_void_p,
                                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_quantize_e4m3": [_i32, _c_void_p, _i64, _i64, _i64, _i32, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_fp8_forward": [_c_void_p, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p],
+    "bsq_fp8_dgrad": [_c_void_p, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p],
+    "bsq_fp8_grouped_forward": [_c_void_p, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                                _c_void_p, _c_void_p],
+    "bsq_fp8_grouped_dgrad": [_c_void_p, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                              _c_void_p, _c_void_p],
+    "bsq_adamw": [_c_void_p, _i32, _i32, _i32, _i64, _f64, _f64, _f64, _f64, _c_void_p, ctypes.c_uint32, _c_void_p],
     "bsq_status_string": [_i32],
     "bsq_last_error": [],
     "bsq_get_device_error": [ctypes.POINTER(_i32), _c_void_p],
@@ -241,3 +250,154 @@ def grouped_wgrad(grad_out, x, offsets, E, out=None, stream=None):
     _check(lib().bsq_grouped_wgrad(_ptr(grad_out), S, N, x.fmt, _ptr(x.data), _ptr(x.scale), _ptr(x.tensor_scale),
                                    x.cols, _ptr(offsets), E, _ptr(out), _stream(stream)))
     return out
+
+
+def _dense(t, dtypes, what):
+    """t is a contiguous CUDA tensor of one of `dtypes`."""
+    if not t.is_cuda or not t.is_contiguous() or t.dtype not in dtypes:
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is wanted, not "
+                         f"{t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _out(out, shape, dtype, device, stream, what):
+    """`out` checked, or a new tensor that `stream` may use."""
+    if out is not None:
+        _dense(out, (dtype,), what)
+        if tuple(out.shape) != tuple(shape):
+            raise ValueError(f"{what}: shape {tuple(out.shape)}, {tuple(shape)} is wanted")
+        return out
+    out = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        out.record_stream(stream)
+    return out
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_DTYPES = {torch.bfloat16: BSQ_DT_BF16, torch.float32: BSQ_DT_F32}
+
+
+def quantize_e4m3(x, block_rows=1, codes=None, scale=None, stream=None):
+    """(codes u8, scale f32) of x (BF16 or float32, [rows, cols] or [batch, rows, cols]) in blocks of
+    block_rows x 128, block_rows 1 (activations, gradients) or 128 (weights)."""
+    _dense(x, tuple(_DTYPES), "quantize_e4m3: x")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"quantize_e4m3: x has {x.dim()} dimensions, 2 or 3 are wanted")
+    lead, (rows, cols) = x.shape[:-2], x.shape[-2:]
+    row_blocks = rows if block_rows == 1 else -(-rows // 128)
+    codes = _out(codes, x.shape, torch.uint8, x.device, stream, "quantize_e4m3: codes")
+    scale = _out(scale, (*lead, row_blocks, -(-cols // 128)), torch.float32, x.device, stream, "quantize_e4m3: scale")
+    _check(lib().bsq_quantize_e4m3(_DTYPES[x.dtype], _ptr(x), lead[0] if lead else 1, rows, cols, block_rows, _ptr(codes),
+                                   _ptr(scale), _stream(stream)))
+    return codes, scale
+
+
+def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
+    _dense(codes, _CODES, f"{name}: codes")
+    _dense(scale, (torch.float32,), f"{name}: scale")
+    _dense(w.data, _CODES, f"{name}: w.data")
+    _dense(w.scale, (torch.float32,), f"{name}: w.scale")
+    rows = codes.shape[0]
+    if codes.dim() != 2 or codes.shape[1] != inner or tuple(scale.shape) != (rows, -(-inner // 128)):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} with scale {tuple(scale.shape)}; [rows, {inner}] with "
+                         f"[rows, {-(-inner // 128)}] are wanted")
+    if w.data.numel() != w.batch * w.rows * w.cols or w.scale.numel() != w.batch * -(-w.rows // 128) * -(-w.cols // 128):
+        raise ValueError(f"{name}: w holds {w.data.numel()} codes and {w.scale.numel()} scales for "
+                         f"[{w.batch}, {w.rows}, {w.cols}]")
+    out = _out(out, (rows, outer), torch.bfloat16, codes.device, stream, f"{name}: out")
+    head = (_ptr(codes), _ptr(scale), rows, w.fmt, _ptr(w.data), _ptr(w.scale))
+    if offsets is None:
+        if w.batch != 1:
+            raise ValueError(f"{name}: one weight is wanted, not {w.batch}")
+        _check(getattr(lib(), "bsq_" + name)(*head, w.rows, w.cols, _ptr(out), _stream(stream)))
+    else:
+        _dense(offsets, (torch.int32,), f"{name}: offsets")
+        if offsets.numel() != w.batch:
+            raise ValueError(f"{name}: {offsets.numel()} offsets for {w.batch} experts")
+        _check(getattr(lib(), "bsq_" + name)(*head, w.batch, w.rows, w.cols, _ptr(offsets), _ptr(out), _stream(stream)))
+    return out
+
+
+def fp8_forward(x_codes, x_scale, w, out=None, stream=None):
+    """y[M,N] (BF16) = X W^T of E4M3 operands: X from quantize_e4m3, W packed in 128x128 blocks."""
+    return _fp8("fp8_forward", x_codes, x_scale, w, w.cols, w.rows, None, out, stream)
+
+
+def fp8_dgrad(g_codes, g_scale, w, out=None, stream=None):
+    """grad_x[M,K] (BF16) = G W of E4M3 operands: G = grad_out from quantize_e4m3."""
+    return _fp8("fp8_dgrad", g_codes, g_scale, w, w.rows, w.cols, None, out, stream)
+
+
+def fp8_grouped_forward(x_codes, x_scale, w, offsets, out=None, stream=None):
+    """Per expert e: y[r0:r1] = X[r0:r1] W[e]^T; rows past offsets[-1] untouched."""
+    return _fp8("fp8_grouped_forward", x_codes, x_scale, w, w.cols, w.rows, offsets, out, stream)
+
+
+def fp8_grouped_dgrad(g_codes, g_scale, w, offsets, out=None, stream=None):
+    """Per expert e: grad_x[r0:r1] = G[r0:r1] W[e]; rows past offsets[-1] untouched."""
+    return _fp8("fp8_grouped_dgrad", g_codes, g_scale, w, w.rows, w.cols, offsets, out, stream)
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", _c_void_p), ("grad", _c_void_p), ("m", _c_void_p), ("v", _c_void_p), ("m_scale", _c_void_p),
+                ("v_scale", _c_void_p), ("copy", _c_void_p), ("n", _i64), ("weight_decay", ctypes.c_float),
+                ("counter", ctypes.c_uint32)]
+
+
+class AdamwTable:
+    """The tensors of an optimizer, checked and laid out once; holds references to them."""
+
+    def __init__(self, items, grad_dtype, state_bits, keep):
+        self.items, self.count, self.grad_dtype, self.state_bits, self.keep = items, len(items), grad_dtype, state_bits, keep
+
+
+def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0):
+    """The table `adamw` steps over.  params: float32; grads: all BF16 or all float32; states: float32,
+    or uint8 E4M3 codes with scales of one float32 per 128 elements (new states: zero codes, any
+    scale); copies: BF16 tensors that receive the updated parameters.  weight_decay: one number or
+    one per tensor.  In the random sequence each tensor takes its length rounded up to 128."""
+    n = len(params)
+    s8 = m_scales is not None
+    if (v_scales is not None) != s8:
+        raise ValueError("adamw_table: m_scales and v_scales come together")
+    decays = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+    lists = dict(params=params, grads=grads, ms=ms, vs=vs, weight_decay=decays)
+    if s8:
+        lists.update(m_scales=m_scales, v_scales=v_scales)
+    if copies is not None:
+        lists.update(copies=copies)
+    for name, seq in lists.items():
+        if len(seq) != n:
+            raise ValueError(f"adamw_table: {len(seq)} {name} for {n} params")
+    grad_dtype = grads[0].dtype if n else torch.float32
+    if grad_dtype not in _DTYPES:
+        raise ValueError(f"adamw_table: gradients of {grad_dtype}")
+    wanted = dict(params=(torch.float32,), grads=(grad_dtype,), ms=(torch.uint8,) if s8 else (torch.float32,),
+                  m_scales=(torch.float32,), copies=(torch.bfloat16,))
+    wanted.update(vs=wanted["ms"], v_scales=wanted["m_scales"])
+    items = (_AdamwTensor * n)()
+    counter = 0
+    for i in range(n):
+        size, blocks = params[i].numel(), -(-params[i].numel() // 128)
+        for name, seq in lists.items():
+            if name == "weight_decay":
+                continue
+            _dense(seq[i], wanted[name], f"adamw_table: {name}[{i}]")
+            if seq[i].numel() != (blocks if name.endswith("_scales") else size) or seq[i].device != params[0].device:
+                raise ValueError(f"adamw_table: {name}[{i}] holds {seq[i].numel()} elements on {seq[i].device}; params[{i}] "
+                                 f"has {size}")
+        p = lambda seq: None if seq is None else seq[i].data_ptr()
+        items[i] = _AdamwTensor(p(params), p(grads), p(ms), p(vs), p(m_scales), p(v_scales), p(copies), size, decays[i],
+                                counter & 0xFFFFFFFF)
+        counter += 128 * blocks
+    return AdamwTable(items, _DTYPES[grad_dtype], 8 if s8 else 32, lists)
+
+
+def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, seed=0, stream=None):
+    """One AdamW step over the tensors of `table`, in place; step counts from 1.  grad_scale: a device
+    float32 that multiplies the gradients (clipping, loss scaling), or None."""
+    if grad_scale is not None:
+        _dense(grad_scale, (torch.float32,), "adamw: grad_scale")
+        if grad_scale.numel() != 1:
+            raise ValueError("adamw: grad_scale is one number")
+    _check(lib().bsq_adamw(table.items, table.count, table.grad_dtype, table.state_bits, step, lr, betas[0], betas[1], eps,
+                           _ptr(grad_scale), seed & 0xFFFFFFFF, _stream(stream)))

@@ -1,5 +1,6 @@
 // bsq_api.cu -- the C entry points declared in include/bsq.h: host-side argument
 // validation, status codes, the per-device error word, and dispatch to the kernels.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -130,6 +131,51 @@ bsq_status zero_output(void* out, int64_t bytes, cudaStream_t s, const char* wha
   if (bytes <= 0) return BSQ_OK;
   const cudaError_t e = cudaMemsetAsync(out, 0, static_cast<size_t>(bytes), s);
   if (e != cudaSuccess) return fail(BSQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return BSQ_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The four products of E4M3 operands.  x: codes [S][inner] with a scale per row and 128
+// columns; W: [E][N][K] in 128 x 128 blocks.  E == 0 with null offsets: a dense call.
+bsq_status run_fp8(const char* what, bool dgrad, bool grouped, const void* x, const float* x_scale, int64_t S, int32_t w_fmt,
+                   const void* w, const float* w_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets, void* y,
+                   void* stream) {
+  if (S < 0 || N < 0 || K < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (S > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return fail(BSQ_ERR_UNSUPPORTED, "%s: size above 2^31-1", what);
+  if (grouped) {
+    if (E < 1) return fail(BSQ_ERR_INVALID_ARG, "%s: E must be >= 1", what);
+    if (E > bsq::kMaxExperts) return fail(BSQ_ERR_UNSUPPORTED, "%s: E > %d", what, bsq::kMaxExperts);
+    if (!offsets) return fail(BSQ_ERR_INVALID_ARG, "%s: null offsets", what);
+    if (!aligned4(offsets)) return fail(BSQ_ERR_INVALID_ARG, "%s: offsets not 4-byte aligned", what);
+  }
+  if (w_fmt < BSQ_BF16 || w_fmt > BSQ_FP8_E5M2_TENSOR) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown format %d", what, w_fmt);
+  if (w_fmt != BSQ_FP8_E4M3_B128)
+    return fail(BSQ_ERR_UNSUPPORTED, "%s: W must be E4M3 with a scale per 128 x 128 block", what);
+  bsq_status st = check_packed(what, w_fmt, w, w_scale, nullptr, E, N, K, false);
+  if (st != BSQ_OK) return st;
+  const int64_t inner = dgrad ? N : K, outer = dgrad ? K : N;
+  if (inner % 16) return fail(BSQ_ERR_UNSUPPORTED, "%s: contraction %% 16 != 0 (row pitch must be 16 bytes)", what);
+  if (outer % 8) return fail(BSQ_ERR_UNSUPPORTED, "%s: N %% 8 != 0 (Y row pitch must be 16 bytes)", what);
+  if (S * inner > 0 && (!x || !aligned16(x)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: the first operand's codes are null or not 16-byte aligned", what);
+  if (S * inner > 0 && (!x_scale || !aligned4(x_scale)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: the first operand's scales are null or not 4-byte aligned", what);
+  if (S * outer > 0 && (!y || !aligned16(y))) return fail(BSQ_ERR_INVALID_ARG, "%s: output null or not 16-byte aligned", what);
+  if (S == 0 || outer == 0) return BSQ_OK;
+  if (inner == 0) {
+    if (grouped) return fail(BSQ_ERR_UNSUPPORTED, "%s: an empty contraction with S > 0 (rows to zero depend on offsets)", what);
+    return zero_output(y, S * outer * 2, static_cast<cudaStream_t>(stream), what);
+  }
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::Fp8Args a{dgrad, x, x_scale, w, w_scale, S, N, K, E, grouped ? offsets : nullptr, y, err, sms,
+                 static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if ((bsq::fp8_takes_smallm(a) ? bsq::launch_fp8_smallm(a, &msg) : bsq::launch_fp8(a, &msg)) != 0)
+    return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
   return BSQ_OK;
 }
 
@@ -447,6 +493,95 @@ bsq_status bsq_linear_backward_e5m2(const void* grad_out, int64_t M, int64_t N, 
   if (st != BSQ_OK) return st;
   return bsq_linear_backward(g_deq, M, N, w_fmt, w_data, w_scale, w_tensor_scale, x_fmt, x_data, x_scale,
                              x_tensor_scale, K, needs, grad_x, grad_w, stream);
+}
+
+bsq_status bsq_quantize_e4m3(int32_t dtype, const void* x, int64_t batch, int64_t rows, int64_t cols, int32_t block_rows,
+                             void* codes, float* scale, void* stream) {
+  const char* what = "bsq_quantize_e4m3";
+  if (dtype != BSQ_DT_BF16 && dtype != BSQ_DT_F32) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown type %d", what, dtype);
+  if (batch < 0 || rows < 0 || cols < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (block_rows != 1 && block_rows != 128) return fail(BSQ_ERR_INVALID_ARG, "%s: blocks have 1 or 128 rows, not %d", what, block_rows);
+  if (batch > INT32_MAX || rows > INT32_MAX || cols > INT32_MAX)
+    return fail(BSQ_ERR_UNSUPPORTED, "%s: dimension above 2^31-1", what);
+  if (cols % 16) return fail(BSQ_ERR_UNSUPPORTED, "%s: cols %% 16 != 0 (row pitch must be 16 bytes)", what);
+  if (batch == 0 || rows == 0 || cols == 0) return BSQ_OK;
+  if (!x || !aligned16(x)) return fail(BSQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", what);
+  if (!codes || !aligned16(codes)) return fail(BSQ_ERR_INVALID_ARG, "%s: codes null or not 16-byte aligned", what);
+  if (!scale || !aligned4(scale)) return fail(BSQ_ERR_INVALID_ARG, "%s: scale null or not 4-byte aligned", what);
+  int32_t* err = nullptr;
+  int sms = 0;
+  bsq_status st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::QuantE4m3Args a{dtype, x, batch, rows, cols, block_rows, codes, scale, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_quantize_e4m3(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_fp8_forward(const void* x_codes, const float* x_scale, int64_t M, int32_t w_fmt, const void* w_data,
+                           const float* w_scale, int64_t N, int64_t K, void* y, void* stream) {
+  return run_fp8("bsq_fp8_forward", false, false, x_codes, x_scale, M, w_fmt, w_data, w_scale, 1, N, K, nullptr, y, stream);
+}
+
+bsq_status bsq_fp8_dgrad(const void* g_codes, const float* g_scale, int64_t M, int32_t w_fmt, const void* w_data,
+                         const float* w_scale, int64_t N, int64_t K, void* grad_x, void* stream) {
+  return run_fp8("bsq_fp8_dgrad", true, false, g_codes, g_scale, M, w_fmt, w_data, w_scale, 1, N, K, nullptr, grad_x, stream);
+}
+
+bsq_status bsq_fp8_grouped_forward(const void* x_codes, const float* x_scale, int64_t S, int32_t w_fmt, const void* w_data,
+                                   const float* w_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets, void* y,
+                                   void* stream) {
+  return run_fp8("bsq_fp8_grouped_forward", false, true, x_codes, x_scale, S, w_fmt, w_data, w_scale, E, N, K, offsets, y,
+                 stream);
+}
+
+bsq_status bsq_fp8_grouped_dgrad(const void* g_codes, const float* g_scale, int64_t S, int32_t w_fmt, const void* w_data,
+                                 const float* w_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets, void* grad_x,
+                                 void* stream) {
+  return run_fp8("bsq_fp8_grouped_dgrad", true, true, g_codes, g_scale, S, w_fmt, w_data, w_scale, E, N, K, offsets, grad_x,
+                 stream);
+}
+
+bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits, int64_t step,
+                     double lr, double beta1, double beta2, double eps, const float* grad_scale, uint32_t seed, void* stream) {
+  const char* what = "bsq_adamw";
+  if (count < 0 || (count > 0 && !tensors)) return fail(BSQ_ERR_INVALID_ARG, "%s: count %d with a null or negative list", what, count);
+  if (grad_dtype != BSQ_DT_BF16 && grad_dtype != BSQ_DT_F32)
+    return fail(BSQ_ERR_INVALID_ARG, "%s: unknown gradient type %d", what, grad_dtype);
+  if (state_bits != 8 && state_bits != 32) return fail(BSQ_ERR_INVALID_ARG, "%s: states of 8 or 32 bits, not %d", what, state_bits);
+  if (step < 1) return fail(BSQ_ERR_INVALID_ARG, "%s: step counts from 1", what);
+  if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: betas must be in [0, 1)", what);
+  if (!(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite(lr))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: lr and eps must be finite, eps not negative", what);
+  if (!aligned4(grad_scale)) return fail(BSQ_ERR_INVALID_ARG, "%s: grad_scale not 4-byte aligned", what);
+  const uintptr_t gmask = grad_dtype == BSQ_DT_BF16 ? 1u : 3u, smask = state_bits == 8 ? 0u : 3u;
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const bsq_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: negative length", what, i);
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v) return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: null pointer", what, i);
+    if (state_bits == 8 && (!t.m_scale || !t.v_scale))
+      return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: 8-bit states need m_scale and v_scale", what, i);
+    if (!aligned4(t.param) || (reinterpret_cast<uintptr_t>(t.grad) & gmask) || (reinterpret_cast<uintptr_t>(t.m) & smask) ||
+        (reinterpret_cast<uintptr_t>(t.v) & smask) || !aligned4(t.m_scale) || !aligned4(t.v_scale) ||
+        (reinterpret_cast<uintptr_t>(t.copy) & 1u))
+      return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: a pointer is not aligned to its elements", what, i);
+    if (!std::isfinite(t.weight_decay)) return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: weight_decay not finite", what, i);
+    if (t.n > (static_cast<int64_t>(1) << 40)) return fail(BSQ_ERR_UNSUPPORTED, "%s: tensor %d: above 2^40 elements", what, i);
+    total += t.n;
+  }
+  if (total == 0) return BSQ_OK;
+  int32_t* err = nullptr;
+  int sms = 0;
+  bsq_status st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::AdamwArgs a{tensors, count, grad_dtype, state_bits, step, lr, beta1, beta2, eps, grad_scale, seed,
+                   static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_adamw(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,209 @@
+// bsq_fp8_smallm.cu -- the forward of E4M3 operands for a few token rows (decode), dense and
+// per expert:  y[m, n] = sum_b xs[m, b] ws[n/128, b] sum_{k in b} xc[m, k] wc[n, k].
+//
+// Bound by reading W once.  A CTA owns 32 columns of y (rows of W) and the whole
+// contraction; its 8 warps take every eighth 128-deep block, each thread streaming W
+// straight into the register fragments of mma.m16n8k32 (no shared memory, no barrier
+// between the load and its use).  A fragment wants 4-byte pieces 16 k apart; the order of k
+// inside a block is free as long as both operands share it, so each thread instead takes
+// 16 consecutive bytes of its row for two MMAs, and the token codes are read the same way.
+// Every block's partial sum is scaled into FP32 accumulators; the warps' accumulators are
+// added in warp order through shared memory, so results do not depend on timing.
+#include <cuda_bf16.h>
+
+#include "bsq_internal.h"
+#include "../../include/bsq.h"
+
+namespace bsq {
+
+namespace {
+
+constexpr int kWarpsS = 8;
+constexpr int kColsS = 32;              // columns of y per CTA
+constexpr int kPadS = kColsS + 4;       // row pitch of the reduction buffer: conflict-free fragment writes
+
+struct Fp8SmallParams {
+  const uint8_t* x;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  __nv_bfloat16* y;
+  const int32_t* offsets;
+  int32_t* err;
+  int32_t S, N, K, E, kblocks;
+};
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// W is read once: kept out of L1 so that the token codes stay there.
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// NT: groups of 8 tokens per pass over W.
+template <int NT>
+__global__ void __launch_bounds__(kWarpsS * 32) fp8_smallm_kernel(const Fp8SmallParams p) {
+  __shared__ float red[kWarpsS][8 * NT][kPadS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int e = blockIdx.y;
+  int r0 = 0, r1 = p.S;
+  if (p.offsets) {
+    r0 = e > 0 ? __ldg(p.offsets + e - 1) : 0;
+    r1 = __ldg(p.offsets + e);
+    int bad = 0;
+    for (int i = tid; i < p.E; i += kWarpsS * 32) {
+      const int a = i > 0 ? __ldg(p.offsets + i - 1) : 0, b = __ldg(p.offsets + i);
+      bad |= a < 0 || b < a || b > p.S;
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0 && blockIdx.x == 0 && e == 0) atomicCAS(p.err, 0, BSQ_DEVERR_BAD_OFFSETS);
+      return;
+    }
+  }
+  const int n0 = blockIdx.x * kColsS;
+  const uint8_t* wrow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)   // rows past N: any row, not stored
+    wrow[i] = p.w + (static_cast<int64_t>(e) * p.N + min(n0 + 8 * i + g, p.N - 1)) * p.K + 16 * t;
+  const float* ws = p.ws + (static_cast<int64_t>(e) * ((p.N + 127) >> 7) + (n0 >> 7)) * p.kblocks;
+
+  for (int m0 = r0; m0 < r1; m0 += 8 * NT) {
+    const uint8_t* xrow[NT];
+    const float* xs[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {   // tokens past the last: any token, not stored
+      xrow[j] = p.x + static_cast<int64_t>(min(m0 + 8 * j + g, r1 - 1)) * p.K + 16 * t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        xs[j][i] = p.xs + static_cast<int64_t>(min(m0 + 8 * j + 2 * t + i, r1 - 1)) * p.kblocks;
+    }
+    float acc[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][j][c] = 0.f;
+
+    // the codes of one block: [half of 64 k][row of the fragment]
+    uint4 wv[2][4];
+    auto load_w = [&](int kb) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = kb * 128 + 64 * h;
+        const bool in = k + 16 * t < p.K;   // K % 16 == 0: whole 16-byte pieces
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wv[h][i] = in ? ldg_stream(wrow[i] + k) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    if (warp < p.kblocks) load_w(warp);
+    for (int kb = warp; kb < p.kblocks; kb += kWarpsS) {
+      uint4 cur[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cur[h][i] = wv[h][i];
+      uint4 xv[NT][2];
+      float sx[NT][2];
+      const float sw = __ldg(ws + kb);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = kb * 128 + 64 * h;
+          xv[j][h] = k + 16 * t < p.K ? __ldg(reinterpret_cast<const uint4*>(xrow[j] + k)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sx[j][i] = __ldg(xs[j][i] + kb);
+      }
+      if (kb + kWarpsS < p.kblocks) load_w(kb + kWarpsS);   // the next block's loads fly over this one's products
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 &lo = cur[h][2 * i], &hi = cur[h][2 * i + 1], &x = xv[j][h];
+            mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+            mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+          }
+          const float s0 = sx[j][0] * sw, s1 = sx[j][1] * sw;
+          acc[i][j][0] += c[0] * s0;
+          acc[i][j][1] += c[1] * s1;
+          acc[i][j][2] += c[2] * s0;
+          acc[i][j][3] += c[3] * s1;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        red[warp][8 * j + 2 * t][16 * i + g] = acc[i][j][0];
+        red[warp][8 * j + 2 * t + 1][16 * i + g] = acc[i][j][1];
+        red[warp][8 * j + 2 * t][16 * i + 8 + g] = acc[i][j][2];
+        red[warp][8 * j + 2 * t + 1][16 * i + 8 + g] = acc[i][j][3];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int m = j * 8 + warp;
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpsS; ++w) s += red[w][m][lane];
+      if (m0 + m < r1 && n0 + lane < p.N) p.y[static_cast<int64_t>(m0 + m) * p.N + n0 + lane] = __float2bfloat16_rn(s);
+    }
+    __syncthreads();
+  }
+}
+
+template <int NT>
+int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
+  const dim3 grid(static_cast<unsigned>((a.N + kColsS - 1) / kColsS), static_cast<unsigned>(a.E));
+  fp8_smallm_kernel<NT><<<grid, kWarpsS * 32, 0, a.stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    *msg = cudaGetErrorString(e);
+    return static_cast<int>(e);
+  }
+  return 0;
+}
+
+}  // namespace
+
+bool fp8_takes_smallm(const Fp8Args& a) { return !a.dgrad && (a.offsets ? a.S <= 4 * a.E : a.S <= 32); }
+
+int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
+  Fp8SmallParams p;
+  p.x = static_cast<const uint8_t*>(a.x);
+  p.xs = a.x_scale;
+  p.w = static_cast<const uint8_t*>(a.w);
+  p.ws = a.w_scale;
+  p.y = static_cast<__nv_bfloat16*>(a.y);
+  p.offsets = a.offsets;
+  p.err = a.err;
+  p.S = static_cast<int32_t>(a.S);
+  p.N = static_cast<int32_t>(a.N);
+  p.K = static_cast<int32_t>(a.K);
+  p.E = static_cast<int32_t>(a.E);
+  p.kblocks = static_cast<int32_t>((a.K + 127) / 128);
+  // tokens per pass: all of them when dense; an expert of a decode batch rarely has more than 8
+  const int64_t rows = a.offsets ? 1 : a.S;
+  if (rows <= 8) return launch_typed<1>(p, a, msg);
+  if (rows <= 16) return launch_typed<2>(p, a, msg);
+  return launch_typed<4>(p, a, msg);
+}
+
+}  // namespace bsq

@@ -1,0 +1,187 @@
+// bsq_quant_e4m3.cu -- block quantization to E4M3: 1 x 128 blocks (activations, gradients) or
+// 128 x 128 blocks (weights).
+//
+//   a = max |x| over the block (a zero block takes 448, a smaller one than 2^-100 takes 2^-100)
+//   scale = a / 448,   code = E4M3(x * (448 / a)), nearest even, saturating at +-448
+//
+// One pass: a block lives in registers between its maximum and its codes, so HBM sees the
+// input once, the codes and the scales.  A NaN in a block makes its scale NaN (maxima are
+// taken on the bit patterns, where NaN is above infinity); an infinity makes the scale
+// infinite and its own code NaN.
+#include <cuda_bf16.h>
+
+#include "bsq_internal.h"
+#include "../../include/bsq.h"
+
+namespace bsq {
+
+namespace {
+
+constexpr int kThreadsQ = 256;
+constexpr int kChunks = 4;   // 256-element pieces of a row per warp
+
+// Eight consecutive elements of either input type, as loaded.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  // bit pattern of the largest magnitude, as a float32's
+  __device__ uint32_t amax() const {
+    const uint32_t m = 0x7FFF7FFFu;
+    const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return max(a << 16, a & 0xFFFF0000u);
+  }
+  __device__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ uint32_t amax() const {
+    auto m = [](float x) { return __float_as_uint(x) & 0x7FFFFFFFu; };
+    return max(max(max(m(a.x), m(a.y)), max(m(a.z), m(a.w))), max(max(m(b.x), m(b.y)), max(m(b.z), m(b.w))));
+  }
+  __device__ float2 pair(int i) const {
+    return i == 0 ? make_float2(a.x, a.y) : i == 1 ? make_float2(a.z, a.w) : i == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
+  }
+};
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// a of the definition from the block's largest magnitude.
+__device__ __forceinline__ float block_amax(uint32_t bits) {
+  const float a = __uint_as_float(bits);
+  return bits == 0 ? 448.f : a < 7.888609052210118e-31f ? 7.888609052210118e-31f : a;   // 2^-100; NaN stays
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 encode(const Eight<T>& v, float inv) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = v.pair(i);
+    c[i] = e4m3x2(f.x * inv, f.y * inv);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// 1 x 128 blocks: 16 lanes per block, two blocks per warp and piece, kChunks pieces loaded
+// before the first is reduced.
+template <typename T>
+__global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_rows_kernel(const T* __restrict__ x, int64_t rows, int cols,
+                                                                        int segs, int nblocks, uint8_t* __restrict__ codes,
+                                                                        float* __restrict__ scale) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreadsQ / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = item / segs;
+  if (row >= rows) return;
+  const int c0 = static_cast<int>(item - row * segs) * (256 * kChunks) + lane * 8;
+  const T* xr = x + row * cols;
+  Eight<T> v[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    if (c0 + 256 * i < cols) v[i].load(xr + c0 + 256 * i);   // cols % 16 == 0: whole eights
+    else v[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = c0 + 256 * i;
+    uint32_t m = v[i].amax();
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float a = block_amax(m);
+    if (c < cols) {
+      *reinterpret_cast<uint2*>(codes + row * cols + c) = encode(v[i], __fdiv_rn(448.f, a));
+      if ((lane & 15) == 0) scale[row * nblocks + (c >> 7)] = __fdiv_rn(a, 448.f);
+    }
+  }
+}
+
+// 128 x 128 blocks: one CTA per block, thread t holding eights of rows t / 16 + 16 i.
+template <typename T>
+__global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_tiles_kernel(const T* __restrict__ x, int rows, int cols,
+                                                                         int row_blocks, int col_blocks,
+                                                                         uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  __shared__ uint32_t wm[kThreadsQ / 32];
+  const int64_t tile = blockIdx.x;
+  const int64_t rb_all = tile / col_blocks;              // batch * row_blocks + row block
+  const int cb = static_cast<int>(tile - rb_all * col_blocks);
+  const int64_t b = rb_all / row_blocks;
+  const int rb = static_cast<int>(rb_all - b * row_blocks);
+  const int c = cb * 128 + (threadIdx.x & 15) * 8;
+  const int r0 = rb * 128 + (threadIdx.x >> 4);
+  const int64_t base = (b * rows + r0) * cols + c;
+  Eight<T> v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (c < cols && r0 + 16 * i < rows) v[i].load(x + base + static_cast<int64_t>(16 * i) * cols);
+    else v[i].zero();
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, v[i].amax());
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreadsQ / 32; ++i) m = max(m, wm[i]);
+  const float a = block_amax(m), inv = __fdiv_rn(448.f, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c < cols && r0 + 16 * i < rows)
+      *reinterpret_cast<uint2*>(codes + base + static_cast<int64_t>(16 * i) * cols) = encode(v[i], inv);
+  if (threadIdx.x == 0) scale[tile] = __fdiv_rn(a, 448.f);
+}
+
+template <typename T>
+int launch_typed(const QuantE4m3Args& a, const char** msg) {
+  const T* x = static_cast<const T*>(a.x);
+  uint8_t* codes = static_cast<uint8_t*>(a.codes);
+  const int cols = static_cast<int>(a.cols), nb = (cols + 127) / 128;
+  int64_t grid;
+  if (a.block_rows == 1) {
+    const int segs = (cols + 256 * kChunks - 1) / (256 * kChunks);
+    grid = (a.batch * a.rows * segs + kThreadsQ / 32 - 1) / (kThreadsQ / 32);
+    if (grid <= INT32_MAX)
+      quantize_e4m3_rows_kernel<T><<<static_cast<unsigned>(grid), kThreadsQ, 0, a.stream>>>(x, a.batch * a.rows, cols, segs, nb,
+                                                                                             codes, a.scale);
+  } else {
+    const int rb = static_cast<int>((a.rows + 127) / 128);
+    grid = a.batch * rb * nb;
+    if (grid <= INT32_MAX)
+      quantize_e4m3_tiles_kernel<T><<<static_cast<unsigned>(grid), kThreadsQ, 0, a.stream>>>(
+          x, static_cast<int>(a.rows), cols, rb, nb, codes, a.scale);
+  }
+  if (grid > INT32_MAX) {
+    *msg = "too many blocks";
+    return -1;
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    *msg = cudaGetErrorString(e);
+    return static_cast<int>(e);
+  }
+  return 0;
+}
+
+}  // namespace
+
+int launch_quantize_e4m3(const QuantE4m3Args& a, const char** msg) {
+  return a.dtype == BSQ_DT_BF16 ? launch_typed<__nv_bfloat16>(a, msg) : launch_typed<float>(a, msg);
+}
+
+}  // namespace bsq

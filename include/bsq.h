@@ -264,6 +264,95 @@ bsq_status bsq_linear_backward_e5m2(const void* grad_out, int64_t M, int64_t N, 
                                     uint32_t needs, int32_t margin, void* g_codes, void* g_deq, float* g_step,
                                     float* g_amax, void* grad_x, void* grad_w, void* stream);
 
+/* Element types of bsq_quantize_e4m3's input and bsq_adamw's gradients. */
+typedef enum {
+  BSQ_DT_BF16 = 0,
+  BSQ_DT_F32 = 1
+} bsq_dtype;
+
+/*
+ * bsq_quantize_e4m3 -- block quantization to E4M3: the operands of the bsq_fp8_* products.
+ *   block_rows 1    blocks of 1 x 128 (activations, gradients): scale f32[batch][rows][ceil(cols/128)]
+ *   block_rows 128  blocks of 128 x 128 (weights, BSQ_FP8_E4M3_B128): scale
+ *                   f32[batch][ceil(rows/128)][ceil(cols/128)]
+ * Per block: a = max |x| (a zero block takes 448, so that its scale is 1; a smaller one than
+ * 2^-100 takes 2^-100), scale = a / 448, code = E4M3 of x * (448 / a), nearest even,
+ * saturating to +-448, each step rounded to float32.  A NaN makes its block's scale and
+ * codes NaN, an infinity its block's scale infinite and its own code NaN.
+ * x: dtype (bsq_dtype) [batch][rows][cols], 16-byte aligned; codes: u8, same shape, 16-byte
+ * aligned; cols % 16 == 0.  Blocks do not cross a batch entry.
+ */
+bsq_status bsq_quantize_e4m3(int32_t dtype, const void* x, int64_t batch, int64_t rows, int64_t cols,
+                             int32_t block_rows, void* codes, float* scale, void* stream);
+
+/*
+ * bsq_fp8_forward -- y[M][N] = X[M][K] W[N][K]^T of E4M3 operands on the FP8 tensor cores, the
+ * scales applied in float32 to every 128-deep partial sum:
+ *     y[m][n] = sum_b xs[m][b] ws[n/128][b] sum_{k in block b} xc[m][k] wc[n][k]
+ * Accumulated in FP32 and rounded once to BF16 (the entry points above decode to BF16
+ * before they multiply; these multiply the codes).
+ * x_codes: u8[M][K], x_scale: f32[M][ceil(K/128)] (bsq_quantize_e4m3, block_rows 1);
+ * W: [N][K] in w_fmt, which must be BSQ_FP8_E4M3_B128.  K % 16 == 0, N % 8 == 0; codes, W's
+ * scales and y 16-byte aligned, x_scale 4-byte.  y: bf16[M][N], fully written; K == 0 gives zeros.
+ * M <= 32 takes a kernel that streams W once for all its rows.
+ */
+bsq_status bsq_fp8_forward(const void* x_codes, const float* x_scale, int64_t M, int32_t w_fmt, const void* w_data,
+                           const float* w_scale, int64_t N, int64_t K, void* y, void* stream);
+
+/*
+ * bsq_fp8_dgrad -- the input gradient of that product with a quantized grad_out:
+ *     grad_x[m][k] = sum_b gs[m][b] ws[b][k/128] sum_{n in block b} gc[m][n] wc[n][k]
+ * g_codes: u8[M][N], g_scale: f32[M][ceil(N/128)]; the same W; grad_x: bf16[M][K], fully written.
+ * N % 16 == 0, K % 16 == 0.  (The weight gradient takes the BF16 X: bsq_linear_wgrad.)
+ */
+bsq_status bsq_fp8_dgrad(const void* g_codes, const float* g_scale, int64_t M, int32_t w_fmt, const void* w_data,
+                         const float* w_scale, int64_t N, int64_t K, void* grad_x, void* stream);
+
+/*
+ * bsq_fp8_grouped_forward, bsq_fp8_grouped_dgrad -- the two products per expert: rows
+ * [offsets[e-1] or 0, offsets[e]) against W[e].  W: [E][N][K]; offsets, rows past
+ * offsets[E-1] (never written) and the limits on E are those of bsq_grouped_dgrad; an empty
+ * contraction is BSQ_ERR_UNSUPPORTED.  A forward of S <= 4 E rows takes the few-rows kernel.
+ */
+bsq_status bsq_fp8_grouped_forward(const void* x_codes, const float* x_scale, int64_t S, int32_t w_fmt,
+                                   const void* w_data, const float* w_scale, int64_t E, int64_t N, int64_t K,
+                                   const int32_t* offsets, void* y, void* stream);
+bsq_status bsq_fp8_grouped_dgrad(const void* g_codes, const float* g_scale, int64_t S, int32_t w_fmt,
+                                 const void* w_data, const float* w_scale, int64_t E, int64_t N, int64_t K,
+                                 const int32_t* offsets, void* grad_x, void* stream);
+
+/* One tensor of bsq_adamw (pointers: device). */
+typedef struct {
+  void* param;           /* f32[n], updated */
+  const void* grad;      /* bf16[n] or f32[n] (grad_dtype) */
+  void* m;               /* first moment, updated: f32[n], or u8[n] E4M3 codes */
+  void* v;               /* second moment, updated: f32[n], or u8[n] E4M3 codes of its square root */
+  float* m_scale;        /* 8-bit states: f32[ceil(n/128)], updated; else unused */
+  float* v_scale;
+  void* copy;            /* bf16[n] copy of the updated param, or NULL */
+  int64_t n;
+  float weight_decay;
+  uint32_t counter;      /* 8-bit states: place of the tensor's first element in the random sequence */
+} bsq_adamw_tensor;
+
+/*
+ * bsq_adamw -- one AdamW step over many tensors (one launch per 256):
+ *     g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *     param = param (1 - lr weight_decay)
+ *             - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32, each operation rounded by itself.  state_bits 8: m and sqrt(v) are kept as
+ * E4M3 codes with a scale per 128 elements (bsq_quantize_e4m3's rule), the new codes rounded
+ * at random from a hash of (seed + step * 0x7F4A7C15, counter + index): the same arguments
+ * give the same codes.  A sqrt(v) above zero keeps at least the smallest code above zero.
+ * tensors: HOST array, read during the call; tensors of n == 0 are skipped.  Pointers need
+ * their elements' alignment; 32-byte aligned ones (16 for bf16, 8 for codes) are faster.
+ * The tensors must not overlap.  step counts from 1; betas in [0, 1).  grad_scale: device
+ * f32, or NULL for 1 (gradient clipping or loss scaling without a host read).
+ */
+bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits,
+                     int64_t step, double lr, double beta1, double beta2, double eps, const float* grad_scale,
+                     uint32_t seed, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* bsq_status_string(int32_t status);
 
