@@ -14,14 +14,20 @@
 // W is stored [N][K].  The forward contracts over its contiguous axis (a K-major B
 // operand), dgrad over its rows (MN-major): one kernel, two descriptors, no transpose.
 //
-// Pair tile: 256 rows (128 per CTA of a cta_group::2 pair) by BN output columns.  Per CTA,
-// 10 warps:
+// Tile: 128 rows by BN output columns, one CTA per SM, 12 warps:
 //   warps 0-7   promotion and epilogue: TMEM lanes 32 (w % 4).., output columns half w / 4
-//   warp 8      TMA producer: 128 x 128 bytes of the first operand, BN/2 x 128 of W's
-//   warp 9      even CTA: MMA issuer; odd CTA: relays "operands landed" to it
-// A 128-deep block of BN = 256 takes 512 tensor-core cycles per SM at the FP8 rate; its
-// promotion is 64 packed FMAs and 4 TMEM loads per thread, about half of that, so two
-// TMEM buffers keep the tensor cores fed.
+//   warp 8      TMA producer: 128 x 128 bytes of the first operand, BN x 128 of W's
+//   warp 9      MMA issuer
+//   warps 10-11 scales: xs * ws of each k-block's rows and column halves, into shared memory
+// A 128-deep block of BN = 256 takes 512 tensor-core cycles per SM; its promotion is 64 packed
+// FMAs and 4 TMEM loads per thread, 256 cycles of each SM quarter's FMA pipe.  What bounds
+// the kernel is the hand-over of the accumulators: TMEM holds two of them (2 x 256
+// columns), and a k-block takes about 1000 cycles from MMA to promotion and back.  Measured,
+// M = 8192, N = 14336, K = 5120: 500 us, 2.4 PFLOP/s (1.26 of the measured BF16 burst
+// rate); without the promotion's FMAs 454 us, without the MMAs and TMA loads 403 us.
+// Tried and slower there: CTA pairs of 256 x 256 (585 us: the hand-over crosses SMs), two
+// 128-column accumulators a k-block (504 to 631 us), 16 promotion warps (513 us), one scale
+// load per thread in the promotion loop instead of the scale warps (531 us).
 #include <atomic>
 #include <cstdlib>
 
@@ -40,25 +46,26 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const voi
 
 namespace {
 
-constexpr int kThreads8 = 320;
-constexpr int kPair8 = 2;
-constexpr uint16_t kPairMask8 = 3;
+constexpr int kThreads8 = 384;
+constexpr int kLaunchRegs = 168;            // registers per thread at launch (65536 / 384, in eights)
+constexpr int kPromoteRegs = 216, kOtherRegs = 72;
+static_assert(256 * kPromoteRegs + 128 * kOtherRegs <= kThreads8 * kLaunchRegs, "register split");
 constexpr int kRows8 = 128;                 // rows of the first operand per CTA
 constexpr int kDepth = 128;                 // contraction per k-block: one scale block, 128 bytes of codes
 constexpr int kABytes = kRows8 * kDepth;    // 16 KB
 constexpr int kTmemCols8 = 512;
-constexpr int kPromoteWarps = 8;
-constexpr int kMaxStages8 = 8;
+constexpr int kPromoteWarps = 8, kScaleWarps = 2;
+constexpr int kMaxStages8 = 6;
 constexpr int kMaxBufs8 = 4;
 
-// BN: output columns of a pair tile.  MN: W is contracted over its rows (dgrad).
+// BN: output columns of a tile.  MN: W is contracted over its rows (dgrad).
 template <int BN, bool MN>
 struct Fp8Cfg {
-  static constexpr int kBBytes = MN ? kDepth * 128 : (BN / 2) * kDepth;   // this CTA's half of W's tile
+  static constexpr int kBBytes = BN * kDepth;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 8;
-  static constexpr int kBufs = kTmemCols8 / BN < kMaxBufs8 ? kTmemCols8 / BN : kMaxBufs8;
-  static constexpr int kCols = BN / 2;               // output columns of one promotion warp
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kBufs = kTmemCols8 / BN;         // accumulators in TMEM
+  static constexpr int kCols = BN / 2;                  // output columns of one promotion warp
   static constexpr int kRing = kStages * kStage;
 };
 
@@ -73,20 +80,19 @@ struct Fp8Params {
   int32_t S, O, E;
   int32_t kblocks, num_nt;
   uint64_t timeout_ns;
-  int32_t drop_announce;       // test hook: the odd CTA's relay never announces a stage
+  int32_t drop_announce;       // test hook: the producer never requests a stage's operands
 };
 
 struct Fp8Shared {
-  uint64_t full[kMaxStages8];       // this CTA's tiles of the stage have landed
-  uint64_t peer_full[kMaxStages8];  // even CTA: the odd CTA's have
+  uint64_t full[kMaxStages8];
   uint64_t empty[kMaxStages8];
-  uint64_t tmem_full[kMaxBufs8];
-  uint64_t tmem_empty[kMaxBufs8];   // even CTA: 8 arrivals, and 4 bytes from each of the odd CTA's 8 warps
+  uint64_t tmem_full[kMaxBufs8];    // the accumulator is complete and its scales are stored
+  uint64_t tmem_empty[kMaxBufs8];
   uint64_t drain;
+  float scale[kMaxBufs8][2][kRows8];   // of an accumulator: column half, row
   uint32_t tmem_base;
-  uint32_t sink;
   uint32_t abort_flag;
-  int32_t total_mt;                 // row tiles of all experts; -1: bad offsets
+  int32_t total_mt;                 // row tiles of all experts; none when the offsets are bad
   int32_t mt_start[kMaxExperts + 1];   // row tiles before expert e
 };
 
@@ -96,22 +102,46 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bo
          | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+
 // The four MMAs (K = 32 each) of one 128-deep block into a fresh accumulator: A K-major,
-// advancing 32 bytes a step; B by BSTEP descriptor units.
+// advancing 32 bytes a step; B by BSTEP descriptor units.  Called by a converged warp, issued
+// by its elected lane: the operands stay in uniform registers.
 template <uint32_t BSTEP>
-__device__ __forceinline__ void umma_e4m3_pair_k128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+__device__ __forceinline__ void umma_e4m3_k128(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                    uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 e, %7, 0;\n\t"
       "setp.ne.b32 p, %3, %3;\n\t"
       "setp.eq.b32 q, %3, %3;\n\t"
       "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
       "add.s64 b1, %2, %4;\n\tadd.s64 b2, %2, %5;\n\tadd.s64 b3, %2, %6;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, q;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP), "r"(elected)
       : "memory");
+}
+// Arrive on the CTA's barrier when every MMA the elected lane issued so far has completed.
+__device__ __forceinline__ void umma_commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 // As tmem_ld_32x32b_x16_wait, 32 columns.
@@ -130,14 +160,87 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32_wait(uint32_t taddr, uint32_t
       : "memory");
 }
 
+// Bounded wait; false when the CTA aborted or the limit ran out, which then aborts it.  The
+// first polls come without a timer read, and nothing here is a call, around which the
+// promotion warps' accumulators would be spilled.
+__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
+                                      uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1u;
+      record_error(err, BSQ_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+// The promotion warps' wait, in a few instructions.  What they wait for is the MMA warp's and
+// the scale warps', whose own waits keep the time: they leave when the CTA has aborted, or
+// after a poll count that no run reaches.
+__device__ __forceinline__ bool wait8_promote(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+#pragma unroll 1
+  for (uint32_t i = 1; i < (1u << 28); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 0 && *abort_flag) break;
+  }
+  return false;
+}
+
 // acc += p * s on a pair of FP32 values.
 __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s2) {
-  asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
+  asm volatile("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
       : "+l"(acc)
       : "r"(p0), "r"(p1), "l"(s2));
 }
 
-// One pair tile: the expert and its rows, and the first output column.
+// Load the next 32 columns from TMEM and, while they fly, acc += cur * s over the current
+// ones.  One statement, ended by the wait, for the reason tmem_ld_32x32b_x16_wait gives.
+__device__ __forceinline__ void tmem_ld_x32_fma(uint32_t taddr, uint32_t (&next)[32], uint64_t* acc, const uint32_t (&cur)[32],
+                                                uint64_t s2) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .b64 p;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%80];\n\t"
+      "mov.b64 p, {%48, %49};\n\tfma.rn.f32x2 %32, p, %81, %32;\n\t"
+      "mov.b64 p, {%50, %51};\n\tfma.rn.f32x2 %33, p, %81, %33;\n\t"
+      "mov.b64 p, {%52, %53};\n\tfma.rn.f32x2 %34, p, %81, %34;\n\t"
+      "mov.b64 p, {%54, %55};\n\tfma.rn.f32x2 %35, p, %81, %35;\n\t"
+      "mov.b64 p, {%56, %57};\n\tfma.rn.f32x2 %36, p, %81, %36;\n\t"
+      "mov.b64 p, {%58, %59};\n\tfma.rn.f32x2 %37, p, %81, %37;\n\t"
+      "mov.b64 p, {%60, %61};\n\tfma.rn.f32x2 %38, p, %81, %38;\n\t"
+      "mov.b64 p, {%62, %63};\n\tfma.rn.f32x2 %39, p, %81, %39;\n\t"
+      "mov.b64 p, {%64, %65};\n\tfma.rn.f32x2 %40, p, %81, %40;\n\t"
+      "mov.b64 p, {%66, %67};\n\tfma.rn.f32x2 %41, p, %81, %41;\n\t"
+      "mov.b64 p, {%68, %69};\n\tfma.rn.f32x2 %42, p, %81, %42;\n\t"
+      "mov.b64 p, {%70, %71};\n\tfma.rn.f32x2 %43, p, %81, %43;\n\t"
+      "mov.b64 p, {%72, %73};\n\tfma.rn.f32x2 %44, p, %81, %44;\n\t"
+      "mov.b64 p, {%74, %75};\n\tfma.rn.f32x2 %45, p, %81, %45;\n\t"
+      "mov.b64 p, {%76, %77};\n\tfma.rn.f32x2 %46, p, %81, %46;\n\t"
+      "mov.b64 p, {%78, %79};\n\tfma.rn.f32x2 %47, p, %81, %47;\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=&r"(next[0]), "=&r"(next[1]), "=&r"(next[2]), "=&r"(next[3]), "=&r"(next[4]), "=&r"(next[5]), "=&r"(next[6]), "=&r"(next[7]),
+        "=&r"(next[8]), "=&r"(next[9]), "=&r"(next[10]), "=&r"(next[11]), "=&r"(next[12]), "=&r"(next[13]), "=&r"(next[14]), "=&r"(next[15]),
+        "=&r"(next[16]), "=&r"(next[17]), "=&r"(next[18]), "=&r"(next[19]), "=&r"(next[20]), "=&r"(next[21]), "=&r"(next[22]), "=&r"(next[23]),
+        "=&r"(next[24]), "=&r"(next[25]), "=&r"(next[26]), "=&r"(next[27]), "=&r"(next[28]), "=&r"(next[29]), "=&r"(next[30]), "=&r"(next[31]),
+        "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7]),
+        "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]), "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15])
+      : "r"(cur[0]), "r"(cur[1]), "r"(cur[2]), "r"(cur[3]), "r"(cur[4]), "r"(cur[5]), "r"(cur[6]), "r"(cur[7]),
+        "r"(cur[8]), "r"(cur[9]), "r"(cur[10]), "r"(cur[11]), "r"(cur[12]), "r"(cur[13]), "r"(cur[14]), "r"(cur[15]),
+        "r"(cur[16]), "r"(cur[17]), "r"(cur[18]), "r"(cur[19]), "r"(cur[20]), "r"(cur[21]), "r"(cur[22]), "r"(cur[23]),
+        "r"(cur[24]), "r"(cur[25]), "r"(cur[26]), "r"(cur[27]), "r"(cur[28]), "r"(cur[29]), "r"(cur[30]), "r"(cur[31]), "r"(taddr), "l"(s2)
+      : "memory");
+}
+
+// One tile: the expert and its rows, and the first output column.
 struct Tile8 {
   int e, row0, row_end, n0;
 };
@@ -150,16 +253,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing);
   volatile uint32_t* abort_flag = &sh.abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same in every lane
+  const uint32_t elected = elect_one();
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
-      mbar_init(smem_u32(&sh.peer_full[s]), 1);
       mbar_init(smem_u32(&sh.empty[s]), 1);
     }
     for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(smem_u32(&sh.tmem_full[b]), 1);
+      mbar_init(smem_u32(&sh.tmem_full[b]), 1 + kScaleWarps);
       mbar_init(smem_u32(&sh.tmem_empty[b]), kPromoteWarps);
     }
     mbar_init(smem_u32(&sh.drain), 1);
@@ -170,10 +274,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     tma_prefetch_map(&tm_x);
     tma_prefetch_map(&tm_w);
   }
-  if (warp == 9) {
-    tmem_alloc_pair(smem_u32(&sh.tmem_base), kTmemCols8);
-    tmem_relinquish_pair();
-  }
+  if (warp == 9) tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols8);
   if (warp == 0) {
     // Row tiles before each expert, and the offsets' validity: lane l takes experts
     // [l * per, (l + 1) * per).
@@ -185,7 +286,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     for (int e = e0; e < e1; ++e) {
       const int b = end(e);
       if (a < 0 || b < a || b > p.S) bad = 1;
-      sum += (max(b - a, 0) + kPair8 * kRows8 - 1) / (kPair8 * kRows8);
+      sum += (max(b - a, 0) + kRows8 - 1) / kRows8;
       a = b;
     }
     bad = __any_sync(0xffffffffu, bad);
@@ -205,22 +306,18 @@ __global__ void __launch_bounds__(kThreads8, 1)
     for (int e = e0; e < e1; ++e) {
       const int b = end(e);
       sh.mt_start[e] = at;
-      at += (max(b - a, 0) + kPair8 * kRows8 - 1) / (kPair8 * kRows8);
+      at += (max(b - a, 0) + kRows8 - 1) / kRows8;
       a = b;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();
   const uint32_t tmem_base = sh.tmem_base;
   const uint64_t limit = p.timeout_ns;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int cl_id = blockIdx.x / kPair8, n_cl = gridDim.x / kPair8;
   const int total_tiles = sh.total_mt * p.num_nt;
-  uint32_t mma_uses = 0;   // MMA thread: k-blocks issued
 
-  // Tile t: experts in order; within one, row tiles vary fastest, so that concurrent pairs
+  // Tile t: experts in order; within one, row tiles vary fastest, so that concurrent CTAs
   // share W tiles in L2.
   auto tile_of = [&](int t) {
     int lo = 0, hi = p.E - 1;
@@ -232,122 +329,161 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int mts = sh.mt_start[lo + 1] - sh.mt_start[lo];
     const int l = t - sh.mt_start[lo] * p.num_nt;
     const int begin = p.offsets && lo > 0 ? __ldg(p.offsets + lo - 1) : 0;
-    return Tile8{lo, begin + (l % mts) * (kPair8 * kRows8), p.offsets ? __ldg(p.offsets + lo) : p.S, (l / mts) * BN};
+    return Tile8{lo, begin + (l % mts) * kRows8, p.offsets ? __ldg(p.offsets + lo) : p.S, (l / mts) * BN};
   };
 
-  if (warp == 8) {
-    // ===== TMA producer =====
-    if (lane == 0) {
-      uint32_t uc = 0, pend_mask = 0, pend_par = 0;
-      for (int t = cl_id; t < total_tiles && !*abort_flag; t += n_cl) {
-        const Tile8 tl = tile_of(t);
-        const int xrow = tl.row0 + rank * kRows8;
-        const int o0 = tl.n0 + rank * (BN / 2);
-        bool ok = true;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++uc) {
-          const Slot sl = ring_slot<C::kStages>(uc);
-          if (!wait_phase(smem_u32(&sh.empty[sl.idx]), sl.par ^ 1u, abort_flag, p.err, limit)) { ok = false; break; }
-          const uint32_t full = smem_u32(&sh.full[sl.idx]);
-          mbar_arrive_expect_tx(full, C::kStage);
-          pend_mask |= 1u << sl.idx;
-          pend_par = (pend_par & ~(1u << sl.idx)) | (sl.par << sl.idx);
-          const uint32_t dst = smem_u32(smem + sl.idx * C::kStage);
-          tma_load_2d(dst, &tm_x, full, kb * kDepth, xrow);
-          if (MN) tma_load_3d(dst + kABytes, &tm_w, full, o0, kb * kDepth, tl.e);
-          else tma_load_3d(dst + kABytes, &tm_w, full, kb * kDepth, o0, tl.e);
-        }
-        if (!ok) break;
-      }
-      if (*abort_flag) drain_pending<C::kStages>(sh.full, pend_mask, pend_par, kDrainLimitNs);
-    }
-  } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {
-      // ===== MMA issuer =====
-      const uint32_t idesc = idesc_e4m3_f32(kPair8 * kRows8, BN, MN);
-      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem + kABytes), 16, 1024);
-      uint32_t uc = 0;
-      bool ok = true;
-      for (int t = cl_id; ok && t < total_tiles && !*abort_flag; t += n_cl) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++uc) {
-          const Slot sl = ring_slot<C::kStages>(uc);
-          const Slot sb = ring_slot<C::kBufs>(uc);
-          const uint32_t peer = smem_u32(&sh.peer_full[sl.idx]);
-          mbar_arrive_expect_tx(peer, 4);
-          if (!wait_phase<true>(smem_u32(&sh.tmem_empty[sb.idx]), sb.par ^ 1u, abort_flag, p.err, limit) ||
-              !wait_phase(smem_u32(&sh.full[sl.idx]), sl.par, abort_flag, p.err, limit) ||
-              !wait_phase<true>(peer, sl.par, abort_flag, p.err, limit)) {
-            ok = false;
-            break;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ===== TMA producer =====
+      if (lane == 0) {
+        uint32_t st = 0, sp = 0, pend_mask = 0, pend_par = 0;
+        for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+          const Tile8 tl = tile_of(t);
+          bool ok = true;
+#pragma unroll 1
+          for (int kb = 0; kb < p.kblocks; ++kb) {
+            if (!wait8(smem_u32(&sh.empty[st]), sp ^ 1u, abort_flag, p.err, limit)) { ok = false; break; }
+            const uint32_t full = smem_u32(&sh.full[st]);
+            if (p.drop_announce) continue;
+            mbar_arrive_expect_tx(full, C::kStage);
+            const uint32_t dst = smem_u32(smem + st * C::kStage);
+            tma_load_2d(dst, &tm_x, full, kb * kDepth, tl.row0);
+            if (MN) {
+              for (int c = 0; c < BN; c += 128)   // 128 columns a box: one swizzle atom wide
+                tma_load_3d(dst + kABytes + c * kDepth, &tm_w, full, tl.n0 + c, kb * kDepth, tl.e);
+            } else {
+              tma_load_3d(dst + kABytes, &tm_w, full, kb * kDepth, tl.n0, tl.e);
+            }
+            pend_mask |= 1u << st;
+            pend_par = (pend_par & ~(1u << st)) | (sp << st);
+            if (++st == C::kStages) {
+              st = 0;
+              sp ^= 1u;
+            }
           }
+          if (!ok) break;
+        }
+        if (*abort_flag) drain_pending<C::kStages>(sh.full, pend_mask, pend_par, kDrainLimitNs);
+      }
+    } else if (warp == 9) {
+      // ===== MMA issuer: the whole warp walks the loop, its elected lane issues =====
+      const uint32_t idesc = idesc_e4m3_f32(kRows8, BN, MN);
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem + kABytes), 128 * kDepth, 1024);
+      const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+      const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
+      uint32_t st = 0, sp = 0, bi = 0, bp = 1;   // stage and its parity, TMEM buffer and its empty parity
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+#pragma unroll 1
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          ok = wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit) && wait8(full0 + 8 * st, sp, abort_flag, p.err, limit);
+          if (!ok) break;
+          __syncwarp();
           tc_fence_after();
-          umma_e4m3_pair_k128<MN ? 256 : 2>(tmem_base + sb.idx * BN, adesc0 + sl.idx * (C::kStage >> 4),
-                                            bdesc0 + sl.idx * (C::kStage >> 4), idesc);
-          umma_commit_pair(smem_u32(&sh.tmem_full[sb.idx]), kPairMask8);
-          umma_commit_pair(smem_u32(&sh.empty[sl.idx]), kPairMask8);
-          ++mma_uses;
+          umma_e4m3_k128<MN ? 256 : 2>(elected, tmem_base + bi * BN, adesc0 + st * (C::kStage >> 4),
+                                       bdesc0 + st * (C::kStage >> 4), idesc);
+          umma_commit(elected, tfull0 + 8 * bi);
+          umma_commit(elected, empty0 + 8 * st);
+          if (++bi == C::kBufs) {
+            bi = 0;
+            bp ^= 1u;
+          }
+          if (++st == C::kStages) {
+            st = 0;
+            sp ^= 1u;
+          }
         }
       }
-    } else if (lane == 0) {
-      // ===== operands-landed relay of the odd CTA =====
-      uint32_t uc = 0;
+    } else {
+      // ===== scales: two rows a thread; a k-block ahead of its accumulator =====
+      const int i = (warp - 10) * 32 + lane;
+      const uint32_t tempty0 = smem_u32(&sh.tmem_empty[0]), tfull0 = smem_u32(&sh.tmem_full[0]);
+      uint32_t bi = 0, bp = 1;
       bool ok = true;
-      for (int t = cl_id; ok && t < total_tiles && !*abort_flag; t += n_cl)
-        for (int kb = 0; kb < p.kblocks; ++kb, ++uc) {
-          const Slot sl = ring_slot<C::kStages>(uc);
-          if (!wait_phase(smem_u32(&sh.full[sl.idx]), sl.par, abort_flag, p.err, limit)) { ok = false; break; }
-          if (!p.drop_announce) st_async_tx_rank(smem_u32(&sh.sink), smem_u32(&sh.peer_full[sl.idx]), 0);
+      for (int t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+        const Tile8 tl = tile_of(t);
+        // rows past the expert's last and columns past the last block: not stored, any scale does
+        const float* xs0 = p.xs + static_cast<int64_t>(min(tl.row0 + i, tl.row_end - 1)) * p.xs_ld;
+        const float* xs1 = p.xs + static_cast<int64_t>(min(tl.row0 + i + 64, tl.row_end - 1)) * p.xs_ld;
+        const float* ws0 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(tl.n0 >> 7) * p.ws_o;
+        const float* ws1 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(min(tl.n0 + C::kCols, p.O - 1) >> 7) * p.ws_o;
+#pragma unroll 1
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          const float x0 = __ldg(xs0 + kb), x1 = __ldg(xs1 + kb);
+          const float w0 = __ldg(ws0), w1 = __ldg(ws1);
+          ws0 += p.ws_c;
+          ws1 += p.ws_c;
+          ok = wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit);
+          if (!ok) break;
+          sh.scale[bi][0][i] = x0 * w0;
+          sh.scale[bi][0][i + 64] = x1 * w0;
+          sh.scale[bi][1][i] = x0 * w1;
+          sh.scale[bi][1][i + 64] = x1 * w1;
+          __syncwarp();
+          if (elected) mbar_arrive(tfull0 + 8 * bi);
+          if (++bi == C::kBufs) {
+            bi = 0;
+            bp ^= 1u;
+          }
         }
+      }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
     // ===== promotion and epilogue: lane = output row, kCols consecutive columns =====
     const int q = warp & 3, h = warp >> 2;
-    uint32_t uc = 0;
-    bool ok = true;
-    for (int t = cl_id; t < total_tiles && !*abort_flag; t += n_cl) {
+    constexpr int kChunks = C::kCols / 32;   // loads of 32 columns; even, so that v[0] starts every k-block
+    static_assert(kChunks % 2 == 0, "register double buffer");
+    uint32_t bi = 0, bp = 0;   // TMEM buffer and its parity
+    const uint32_t scale0 = smem_u32(&sh.scale[0][h][q * 32 + lane]);
+    const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
+    const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * C::kCols;
+    for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
       const Tile8 tl = tile_of(t);
-      const int row = tl.row0 + rank * kRows8 + q * 32 + lane;
+      const int row = tl.row0 + q * 32 + lane;
       const int col0 = tl.n0 + h * C::kCols;
       const bool valid = row < tl.row_end;
-      const float* xs = p.xs + static_cast<int64_t>(valid ? row : tl.row_end - 1) * p.xs_ld;
-      // columns past the last scale block are not stored: any scale does
-      const int ob = min(col0, p.O - 1) >> 7;
-      const float* ws = p.ws + tl.e * p.ws_e + static_cast<int64_t>(ob) * p.ws_o;
       uint64_t acc[C::kCols / 2];
 #pragma unroll
       for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
-      float sx = __ldg(xs), sw = __ldg(ws);
-      for (int kb = 0; kb < p.kblocks; ++kb, ++uc) {
-        const Slot sb = ring_slot<C::kBufs>(uc);
-        const float s = sx * sw;
-        if (kb + 1 < p.kblocks) {
-          sx = __ldg(xs + kb + 1);
-          sw = __ldg(ws + static_cast<int64_t>(kb + 1) * p.ws_c);
-        }
-        uint64_t s2;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(__float_as_uint(s)));
-        ok = wait_phase(smem_u32(&sh.tmem_full[sb.idx]), sb.par, abort_flag, p.err, limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      uint32_t v[2][32];
+      uint64_t s2;   // the k-block's scale, twice
+      // the next accumulator and its scale
+      auto arrived = [&]() {
+        const bool there = wait8_promote(tfull0 + 8 * bi, bp, abort_flag);
         tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + sb.idx * BN + h * C::kCols;
+        asm volatile("{\n\t.reg .b32 s;\n\tld.shared.b32 s, [%1];\n\tmov.b64 %0, {s, s};\n\t}"
+                     : "=l"(s2)
+                     : "r"(scale0 + bi * (2 * kRows8 * 4))
+                     : "memory");
+        return there;
+      };
+      if (!arrived()) goto promoted;   // aborted: nothing is stored
+      tmem_ld_32x32b_x32_wait(trow + bi * BN, v[0]);
+#pragma unroll 1
+      for (int left = p.kblocks; left > 0; --left) {
+        const uint32_t at = trow + bi * BN;
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32_wait(taddr + c * 32, v);
-          if (c + 1 == C::kCols / 32) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.tmem_empty[sb.idx]), 4);
-              else st_async_tx_rank(smem_u32(&sh.sink), smem_u32(&sh.tmem_empty[sb.idx]), 0);
-            }
-          }
+        for (int c = 0; c + 1 < kChunks; ++c) tmem_ld_x32_fma(at + (c + 1) * 32, v[(c + 1) & 1], acc + c * 16, v[c & 1], s2);
+        // every column is in registers: the TMEM is free before the last are used
+        const uint64_t s = s2;
+        tc_fence_before();
+        __syncwarp();
+        if (elected) mbar_arrive(tempty0 + 8 * bi);
+        if (++bi == C::kBufs) {
+          bi = 0;
+          bp ^= 1u;
+        }
+        if (left > 1) {
+          if (!arrived()) goto promoted;
+          tmem_ld_x32_fma(trow + bi * BN, v[0], acc + (kChunks - 1) * 16, v[1], s);
+        } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fma_f32x2(acc[c * 16 + j], v[2 * j], v[2 * j + 1], s2);
+          for (int j = 0; j < 16; ++j) fma_f32x2(acc[(kChunks - 1) * 16 + j], v[1][2 * j], v[1][2 * j + 1], s);
         }
       }
-      if (!ok) break;
       if (valid) {
         uint4* o4 = reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + col0);   // O % 8 == 0: 16-byte aligned
 #pragma unroll
@@ -360,36 +496,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
       }
     }
+  promoted:;
   }
 
   // ---------------------------------------------------------------- teardown
   __syncthreads();
-  if (warp == 9 && lane == 0 && rank == 0) {
-    umma_commit_pair(smem_u32(&sh.drain), 1);
-    uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kDrainLimitNs) {
-    }
-    if (!*abort_flag) {
-      // the odd CTA's last asynchronous stores have landed
-      for (uint32_t b = 0; b < static_cast<uint32_t>(C::kBufs); ++b) {
-        const uint32_t uses = (mma_uses + C::kBufs - 1u - b) / C::kBufs;
-        if (uses == 0) continue;
-        t0 = global_timer_ns();
-        while (!mbar_try_wait(smem_u32(&sh.tmem_empty[b]), (uses - 1u) & 1u) && global_timer_ns() - t0 < kDrainLimitNs) {
-        }
-      }
-    }
-  }
-  if (rank == 0 && *abort_flag) {
+  if (warp == 9 && elected) {   // the lane that issued the MMAs: all of them have completed
+    const uint32_t drain = smem_u32(&sh.drain);
+    umma_commit(1u, drain);
     const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < kAbortSettleNs) {
+    while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < kDrainLimitNs) {
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();
-  if (warp == 9) tmem_dealloc_pair(tmem_base, kTmemCols8);
+  if (warp == 9) tmem_dealloc(tmem_base, kTmemCols8);
 }
 
 template <int BN, bool MN>
@@ -409,7 +531,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   {
     const uint64_t dims[3] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.E)};
     const uint64_t strides[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.K) * static_cast<uint64_t>(a.N)};
-    const uint32_t box[3] = {128, MN ? kDepth : BN / 2, 1};
+    const uint32_t box[3] = {128, MN ? kDepth : BN, 1};
     if (!encode_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) {
       *msg = "tensor map encoding failed for W";
       return -1;
@@ -435,7 +557,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   const char* drop = std::getenv("BSQ_TEST_DROP_ANNOUNCE");
   p.drop_announce = drop && drop[0] == '1' ? 1 : 0;
   // an upper bound of the row tiles: the exact count depends on the offsets
-  int64_t mt = (a.S + kPair8 * kRows8 - 1) / (kPair8 * kRows8);
+  int64_t mt = (a.S + kRows8 - 1) / kRows8;
   if (a.offsets) mt += a.E < a.S ? a.E : a.S;
   if (mt * p.num_nt > INT32_MAX - 4096) {
     *msg = "too many output tiles";
@@ -444,34 +566,25 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   static_assert(C::kRing + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
   const size_t smem = static_cast<size_t>(C::kRing) + sizeof(Fp8Shared) + 1024;
   auto kern = bsq_fp8_kernel<BN, MN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kPair8;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads8);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  static std::atomic<int> max_clusters_of[kMaxDevices];
+  static std::atomic<uint64_t> ready;   // devices (one bit each) on which the kernel is set up
   int dev = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
-  int max_clusters = e == cudaSuccess ? max_clusters_of[dev].load() : 0;
-  if (e == cudaSuccess && max_clusters == 0) {
-    cfg.gridDim = dim3(kPair8 * (a.num_sms / kPair8));
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    max_clusters = n > 0 ? n : a.num_sms / kPair8;
-    max_clusters_of[dev].store(max_clusters);
+  if (e == cudaSuccess && !(ready.load() >> dev & 1u)) {
+    // the promotion warps' registers come from the launch's: a build that took fewer would
+    // leave them waiting
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e == cudaSuccess && attr.numRegs != kLaunchRegs) {
+      *msg = "built with another register count than its split needs";
+      return -1;
+    }
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) ready.fetch_or(uint64_t(1) << dev);
   }
-  int64_t clusters = mt * p.num_nt < max_clusters ? mt * p.num_nt : max_clusters;
-  if (clusters < 1) clusters = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kPair8));
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, p);
+  const int64_t tiles = mt * p.num_nt;
+  const int grid = static_cast<int>(tiles < a.num_sms ? tiles : a.num_sms);
+  if (e == cudaSuccess) kern<<<grid, kThreads8, smem, a.stream>>>(tm_x, tm_w, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);
