@@ -254,66 +254,80 @@ def grouped_wgrad(grad_out, x, offsets, E, out=None, stream=None):
 
 def _dense(t, dtypes, what):
     """t is a contiguous CUDA tensor of one of `dtypes`."""
-    if not t.is_cuda or not t.is_contiguous() or t.dtype not in dtypes:
+    if not (t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{what}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is wanted, not "
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
 
 
-def _out(out, shape, dtype, device, stream, what):
-    """`out` checked, or a new tensor that `stream` may use."""
+def _out(out, shape, dtype, like, stream, what):
+    """`out` checked, or a new tensor on `like`'s device that `stream` may use."""
     if out is not None:
         _dense(out, (dtype,), what)
-        if tuple(out.shape) != tuple(shape):
+        if out.shape != torch.Size(shape):
             raise ValueError(f"{what}: shape {tuple(out.shape)}, {tuple(shape)} is wanted")
         return out
-    out = torch.empty(shape, dtype=dtype, device=device)
+    out = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         out.record_stream(stream)
     return out
 
 
+def _raw_stream(stream, like):
+    """The stream's handle; None: the current stream of `like`'s device, without building its object."""
+    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
+
+
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_F32 = (torch.float32,)
 _DTYPES = {torch.bfloat16: BSQ_DT_BF16, torch.float32: BSQ_DT_F32}
 
 
 def quantize_e4m3(x, block_rows=1, codes=None, scale=None, stream=None):
     """(codes u8, scale f32) of x (BF16 or float32, [rows, cols] or [batch, rows, cols]) in blocks of
     block_rows x 128, block_rows 1 (activations, gradients) or 128 (weights)."""
-    _dense(x, tuple(_DTYPES), "quantize_e4m3: x")
-    if x.dim() not in (2, 3):
-        raise ValueError(f"quantize_e4m3: x has {x.dim()} dimensions, 2 or 3 are wanted")
-    lead, (rows, cols) = x.shape[:-2], x.shape[-2:]
-    row_blocks = rows if block_rows == 1 else -(-rows // 128)
-    codes = _out(codes, x.shape, torch.uint8, x.device, stream, "quantize_e4m3: codes")
-    scale = _out(scale, (*lead, row_blocks, -(-cols // 128)), torch.float32, x.device, stream, "quantize_e4m3: scale")
-    _check(lib().bsq_quantize_e4m3(_DTYPES[x.dtype], _ptr(x), lead[0] if lead else 1, rows, cols, block_rows, _ptr(codes),
-                                   _ptr(scale), _stream(stream)))
+    _dense(x, _DTYPES, "quantize_e4m3: x")
+    shape = x.shape
+    if len(shape) == 2:
+        batch, (rows, cols) = 1, shape
+    elif len(shape) == 3:
+        batch, rows, cols = shape
+    else:
+        raise ValueError(f"quantize_e4m3: x has {len(shape)} dimensions, 2 or 3 are wanted")
+    blocks = (rows if block_rows == 1 else (rows + 127) // 128, (cols + 127) // 128)
+    codes = _out(codes, shape, torch.uint8, x, stream, "quantize_e4m3: codes")
+    scale = _out(scale, blocks if len(shape) == 2 else (batch, *blocks), torch.float32, x, stream, "quantize_e4m3: scale")
+    _check(lib().bsq_quantize_e4m3(_DTYPES[x.dtype], x.data_ptr(), batch, rows, cols, block_rows, codes.data_ptr(),
+                                   scale.data_ptr(), _raw_stream(stream, x)))
     return codes, scale
 
 
 def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
-    _dense(codes, _CODES, f"{name}: codes")
-    _dense(scale, (torch.float32,), f"{name}: scale")
-    _dense(w.data, _CODES, f"{name}: w.data")
-    _dense(w.scale, (torch.float32,), f"{name}: w.scale")
-    rows = codes.shape[0]
-    if codes.dim() != 2 or codes.shape[1] != inner or tuple(scale.shape) != (rows, -(-inner // 128)):
+    wd, ws, batch, n, k = w.data, w.scale, w.batch, w.rows, w.cols
+    _dense(codes, _CODES, name)
+    _dense(scale, _F32, name)
+    _dense(wd, _CODES, name)
+    _dense(ws, _F32, name)
+    if not codes.get_device() == scale.get_device() == wd.get_device() == ws.get_device():
+        raise ValueError(f"{name}: operands on different devices")
+    rows, blocks = codes.shape[0], (inner + 127) // 128
+    if codes.shape != (rows, inner) or scale.shape != (rows, blocks):
         raise ValueError(f"{name}: codes {tuple(codes.shape)} with scale {tuple(scale.shape)}; [rows, {inner}] with "
-                         f"[rows, {-(-inner // 128)}] are wanted")
-    if w.data.numel() != w.batch * w.rows * w.cols or w.scale.numel() != w.batch * -(-w.rows // 128) * -(-w.cols // 128):
-        raise ValueError(f"{name}: w holds {w.data.numel()} codes and {w.scale.numel()} scales for "
-                         f"[{w.batch}, {w.rows}, {w.cols}]")
-    out = _out(out, (rows, outer), torch.bfloat16, codes.device, stream, f"{name}: out")
-    head = (_ptr(codes), _ptr(scale), rows, w.fmt, _ptr(w.data), _ptr(w.scale))
+                         f"[rows, {blocks}] are wanted")
+    if wd.numel() != batch * n * k or (w.fmt == BSQ_FP8_E4M3_B128 and
+                                       ws.numel() != batch * ((n + 127) // 128) * ((k + 127) // 128)):
+        raise ValueError(f"{name}: w holds {wd.numel()} codes and {ws.numel()} scales for [{batch}, {n}, {k}]")
+    out = _out(out, (rows, outer), torch.bfloat16, codes, stream, name)
     if offsets is None:
-        if w.batch != 1:
-            raise ValueError(f"{name}: one weight is wanted, not {w.batch}")
-        _check(getattr(lib(), "bsq_" + name)(*head, w.rows, w.cols, _ptr(out), _stream(stream)))
+        if batch != 1:
+            raise ValueError(f"{name}: one weight is wanted, not {batch}")
+        _check(getattr(lib(), "bsq_" + name)(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(),
+                                             n, k, out.data_ptr(), _raw_stream(stream, codes)))
     else:
-        _dense(offsets, (torch.int32,), f"{name}: offsets")
-        if offsets.numel() != w.batch:
-            raise ValueError(f"{name}: {offsets.numel()} offsets for {w.batch} experts")
-        _check(getattr(lib(), "bsq_" + name)(*head, w.batch, w.rows, w.cols, _ptr(offsets), _ptr(out), _stream(stream)))
+        _dense(offsets, (torch.int32,), name)
+        if offsets.numel() != batch:
+            raise ValueError(f"{name}: {offsets.numel()} offsets for {batch} experts")
+        _check(getattr(lib(), "bsq_" + name)(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(),
+                                             batch, n, k, offsets.data_ptr(), out.data_ptr(), _raw_stream(stream, codes)))
     return out
 
 
@@ -348,6 +362,7 @@ class AdamwTable:
 
     def __init__(self, items, grad_dtype, state_bits, keep):
         self.items, self.count, self.grad_dtype, self.state_bits, self.keep = items, len(items), grad_dtype, state_bits, keep
+        self.address, self.like = ctypes.addressof(items), keep["params"][0] if keep["params"] else None
 
 
 def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0):
@@ -396,8 +411,11 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, seed=0
     """One AdamW step over the tensors of `table`, in place; step counts from 1.  grad_scale: a device
     float32 that multiplies the gradients (clipping, loss scaling), or None."""
     if grad_scale is not None:
-        _dense(grad_scale, (torch.float32,), "adamw: grad_scale")
+        _dense(grad_scale, _F32, "adamw: grad_scale")
         if grad_scale.numel() != 1:
             raise ValueError("adamw: grad_scale is one number")
-    _check(lib().bsq_adamw(table.items, table.count, table.grad_dtype, table.state_bits, step, lr, betas[0], betas[1], eps,
-                           _ptr(grad_scale), seed & 0xFFFFFFFF, _stream(stream)))
+    if table.like is None:
+        return
+    _check(lib().bsq_adamw(table.address, table.count, table.grad_dtype, table.state_bits, step, lr, betas[0], betas[1], eps,
+                           None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF,
+                           _raw_stream(stream, table.like)))

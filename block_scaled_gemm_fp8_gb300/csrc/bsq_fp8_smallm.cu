@@ -2,7 +2,7 @@
 // per expert:  y[m, n] = sum_b xs[m, b] ws[n/128, b] sum_{k in b} xc[m, k] wc[n, k].
 //
 // Bound by reading W once.  A CTA owns 32 columns of y (rows of W) and the whole
-// contraction; its 8 warps take every eighth 128-deep block, each thread streaming W
+// contraction; its warps take the 128-deep blocks in turn, each thread streaming W
 // straight into the register fragments of mma.m16n8k32 (no shared memory, no barrier
 // between the load and its use).  A fragment wants 4-byte pieces 16 k apart; the order of k
 // inside a block is free as long as both operands share it, so each thread instead takes
@@ -18,7 +18,6 @@ namespace bsq {
 
 namespace {
 
-constexpr int kWarpsS = 8;
 constexpr int kColsS = 32;              // columns of y per CTA
 constexpr int kPadS = kColsS + 4;       // row pitch of the reduction buffer: conflict-free fragment writes
 
@@ -50,26 +49,25 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
   return v;
 }
 
-// NT: groups of 8 tokens per pass over W.
-template <int NT>
-__global__ void __launch_bounds__(kWarpsS * 32) fp8_smallm_kernel(const Fp8SmallParams p) {
-  __shared__ float red[kWarpsS][8 * NT][kPadS];
+// NT: groups of 8 tokens per pass over W.  WARPS of a CTA; AHEAD: a block's W is loaded while
+// the one before it is multiplied; CTAS an SM shall hold.
+template <int NT, int WARPS, bool AHEAD, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) fp8_smallm_kernel(const Fp8SmallParams p) {
+  __shared__ float red[WARPS][8 * NT][kPadS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int e = blockIdx.y;
-  int r0 = 0, r1 = p.S;
+  int r0 = 0, r1 = p.S, bad = 0;
   if (p.offsets) {
     r0 = e > 0 ? __ldg(p.offsets + e - 1) : 0;
     r1 = __ldg(p.offsets + e);
-    int bad = 0;
-    for (int i = tid; i < p.E; i += kWarpsS * 32) {
+    for (int i = tid; i < p.E; i += WARPS * 32) {
       const int a = i > 0 ? __ldg(p.offsets + i - 1) : 0, b = __ldg(p.offsets + i);
       bad |= a < 0 || b < a || b > p.S;
     }
-    if (__syncthreads_or(bad)) {
-      if (tid == 0 && blockIdx.x == 0 && e == 0) atomicCAS(p.err, 0, BSQ_DEVERR_BAD_OFFSETS);
-      return;
-    }
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0 && blockIdx.x == 0 && e == 0) atomicCAS(p.err, 0, BSQ_DEVERR_BAD_OFFSETS);
+    if (bad || r0 == r1) return;
   }
   const int n0 = blockIdx.x * kColsS;
   const uint8_t* wrow[4];
@@ -97,23 +95,28 @@ __global__ void __launch_bounds__(kWarpsS * 32) fp8_smallm_kernel(const Fp8Small
         for (int c = 0; c < 4; ++c) acc[i][j][c] = 0.f;
 
     // the codes of one block: [half of 64 k][row of the fragment]
-    uint4 wv[2][4];
-    auto load_w = [&](int kb) {
+    auto load_w = [&](int kb, uint4 (&v)[2][4]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = kb * 128 + 64 * h;
         const bool in = k + 16 * t < p.K;   // K % 16 == 0: whole 16-byte pieces
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wv[h][i] = in ? ldg_stream(wrow[i] + k) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) v[h][i] = in ? ldg_stream(wrow[i] + k) : make_uint4(0, 0, 0, 0);
       }
     };
-    if (warp < p.kblocks) load_w(warp);
-    for (int kb = warp; kb < p.kblocks; kb += kWarpsS) {
+    uint4 next[2][4];
+    if (AHEAD && warp < p.kblocks) load_w(warp, next);
+#pragma unroll 1
+    for (int kb = warp; kb < p.kblocks; kb += WARPS) {
       uint4 cur[2][4];
+      if (AHEAD) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cur[h][i] = wv[h][i];
+          for (int i = 0; i < 4; ++i) cur[h][i] = next[h][i];
+      } else {
+        load_w(kb, cur);
+      }
       uint4 xv[NT][2];
       float sx[NT][2];
       const float sw = __ldg(ws + kb);
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kWarpsS * 32) fp8_smallm_kernel(const Fp8Small
 #pragma unroll
         for (int i = 0; i < 2; ++i) sx[j][i] = __ldg(xs[j][i] + kb);
       }
-      if (kb + kWarpsS < p.kblocks) load_w(kb + kWarpsS);   // the next block's loads fly over this one's products
+      if (AHEAD && kb + WARPS < p.kblocks) load_w(kb + WARPS, next);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -157,22 +160,20 @@ __global__ void __launch_bounds__(kWarpsS * 32) fp8_smallm_kernel(const Fp8Small
         red[warp][8 * j + 2 * t + 1][16 * i + 8 + g] = acc[i][j][3];
       }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int m = j * 8 + warp;
+    for (int m = warp; m < 8 * NT; m += WARPS) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarpsS; ++w) s += red[w][m][lane];
+      for (int w = 0; w < WARPS; ++w) s += red[w][m][lane];
       if (m0 + m < r1 && n0 + lane < p.N) p.y[static_cast<int64_t>(m0 + m) * p.N + n0 + lane] = __float2bfloat16_rn(s);
     }
     __syncthreads();
   }
 }
 
-template <int NT>
+template <int NT, int WARPS, bool AHEAD, int CTAS>
 int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
   const dim3 grid(static_cast<unsigned>((a.N + kColsS - 1) / kColsS), static_cast<unsigned>(a.E));
-  fp8_smallm_kernel<NT><<<grid, kWarpsS * 32, 0, a.stream>>>(p);
+  fp8_smallm_kernel<NT, WARPS, AHEAD, CTAS><<<grid, WARPS * 32, 0, a.stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);
@@ -199,11 +200,13 @@ int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
   p.K = static_cast<int32_t>(a.K);
   p.E = static_cast<int32_t>(a.E);
   p.kblocks = static_cast<int32_t>((a.K + 127) / 128);
-  // tokens per pass: all of them when dense; an expert of a decode batch rarely has more than 8
-  const int64_t rows = a.offsets ? 1 : a.S;
-  if (rows <= 8) return launch_typed<1>(p, a, msg);
-  if (rows <= 16) return launch_typed<2>(p, a, msg);
-  return launch_typed<4>(p, a, msg);
+  // Dense: all rows in one pass, few CTAs, so many warps with a block in flight ahead.  Grouped:
+  // an expert of a decode batch rarely has more than 8 rows, and there are CTAs enough to
+  // fill every SM three times over, which keeps more bytes in flight than loading ahead.
+  if (a.offsets) return launch_typed<1, 8, false, 3>(p, a, msg);
+  if (a.S <= 8) return launch_typed<1, 16, true, 1>(p, a, msg);
+  if (a.S <= 16) return launch_typed<2, 16, true, 1>(p, a, msg);
+  return launch_typed<4, 8, false, 2>(p, a, msg);
 }
 
 }  // namespace bsq

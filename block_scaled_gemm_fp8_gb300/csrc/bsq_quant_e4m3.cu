@@ -18,7 +18,7 @@ namespace bsq {
 namespace {
 
 constexpr int kThreadsQ = 256;
-constexpr int kChunks = 4;   // 256-element pieces of a row per warp
+constexpr int kChunks = 2;   // 512-element pieces of a row per warp
 
 // Eight consecutive elements of either input type, as loaded.
 template <typename T>
@@ -79,8 +79,8 @@ __device__ __forceinline__ uint2 encode(const Eight<T>& v, float inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// 1 x 128 blocks: 16 lanes per block, two blocks per warp and piece, kChunks pieces loaded
-// before the first is reduced.
+// 1 x 128 blocks: 8 lanes of 16 elements per block, four blocks per warp and piece, kChunks
+// pieces loaded before the first is reduced.
 template <typename T>
 __global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_rows_kernel(const T* __restrict__ x, int64_t rows, int cols,
                                                                         int segs, int nblocks, uint8_t* __restrict__ codes,
@@ -89,24 +89,29 @@ __global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_rows_kernel(const T* 
   const int lane = threadIdx.x & 31;
   const int64_t row = item / segs;
   if (row >= rows) return;
-  const int c0 = static_cast<int>(item - row * segs) * (256 * kChunks) + lane * 8;
+  const int c0 = static_cast<int>(item - row * segs) * (512 * kChunks) + lane * 16;
   const T* xr = x + row * cols;
-  Eight<T> v[kChunks];
+  Eight<T> v[kChunks][2];
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    if (c0 + 256 * i < cols) v[i].load(xr + c0 + 256 * i);   // cols % 16 == 0: whole eights
-    else v[i].zero();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (c0 + 512 * i < cols) v[i][h].load(xr + c0 + 512 * i + 8 * h);   // cols % 16 == 0: whole sixteens
+      else v[i][h].zero();
+    }
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int c = c0 + 256 * i;
-    uint32_t m = v[i].amax();
+    const int c = c0 + 512 * i;
+    uint32_t m = max(v[i][0].amax(), v[i][1].amax());
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = 4; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float a = block_amax(m);
     if (c < cols) {
-      *reinterpret_cast<uint2*>(codes + row * cols + c) = encode(v[i], __fdiv_rn(448.f, a));
-      if ((lane & 15) == 0) scale[row * nblocks + (c >> 7)] = __fdiv_rn(a, 448.f);
+      const float inv = __fdiv_rn(448.f, a);
+      const uint2 lo = encode(v[i][0], inv), hi = encode(v[i][1], inv);
+      *reinterpret_cast<uint4*>(codes + row * cols + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if ((lane & 7) == 0) scale[row * nblocks + (c >> 7)] = __fdiv_rn(a, 448.f);
     }
   }
 }
@@ -154,7 +159,7 @@ int launch_typed(const QuantE4m3Args& a, const char** msg) {
   const int cols = static_cast<int>(a.cols), nb = (cols + 127) / 128;
   int64_t grid;
   if (a.block_rows == 1) {
-    const int segs = (cols + 256 * kChunks - 1) / (256 * kChunks);
+    const int segs = (cols + 512 * kChunks - 1) / (512 * kChunks);
     grid = (a.batch * a.rows * segs + kThreadsQ / 32 - 1) / (kThreadsQ / 32);
     if (grid <= INT32_MAX)
       quantize_e4m3_rows_kernel<T><<<static_cast<unsigned>(grid), kThreadsQ, 0, a.stream>>>(x, a.batch * a.rows, cols, segs, nb,
