@@ -57,6 +57,7 @@ constexpr int kTmemCols8 = 512;
 constexpr int kPromoteWarps = 8, kScaleWarps = 2;
 constexpr int kMaxStages8 = 6;
 constexpr int kMaxBufs8 = 4;
+constexpr int kMaxSplit = 4;                // clusters of 8 do not all fit the SMs at once
 
 // BN: output columns of a tile.  MN: W is contracted over its rows (dgrad).
 template <int BN, bool MN>
@@ -79,6 +80,7 @@ struct Fp8Params {
   int32_t* err;
   int32_t S, O, E;
   int32_t kblocks, num_nt;
+  int32_t split;               // CTAs of a cluster that share a tile's contraction; 1: none
   uint64_t timeout_ns;
   int32_t drop_announce;       // test hook: the producer never requests a stage's operands
 };
@@ -316,6 +318,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
   const uint32_t tmem_base = sh.tmem_base;
   const uint64_t limit = p.timeout_ns;
   const int total_tiles = sh.total_mt * p.num_nt;
+  // With a split, the CTAs of a cluster take one tile, each a part of its k-blocks; without,
+  // a CTA takes tiles until none is left.
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile0 = blockIdx.x / p.split, tile_step = p.split > 1 ? total_tiles : gridDim.x;
+  const int kb0 = p.kblocks * rank / p.split, kb1 = p.kblocks * (rank + 1) / p.split;
 
   // Tile t: experts in order; within one, row tiles vary fastest, so that concurrent CTAs
   // share W tiles in L2.
@@ -338,11 +345,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
       // ===== TMA producer =====
       if (lane == 0) {
         uint32_t st = 0, sp = 0, pend_mask = 0, pend_par = 0;
-        for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+        for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
           const Tile8 tl = tile_of(t);
           bool ok = true;
 #pragma unroll 1
-          for (int kb = 0; kb < p.kblocks; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!wait8(smem_u32(&sh.empty[st]), sp ^ 1u, abort_flag, p.err, limit)) { ok = false; break; }
             const uint32_t full = smem_u32(&sh.full[st]);
             if (p.drop_announce) continue;
@@ -375,9 +382,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
       const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
       uint32_t st = 0, sp = 0, bi = 0, bp = 1;   // stage and its parity, TMEM buffer and its empty parity
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+      for (int t = tile0; ok && t < total_tiles && !*abort_flag; t += tile_step) {
 #pragma unroll 1
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit) && wait8(full0 + 8 * st, sp, abort_flag, p.err, limit);
           if (!ok) break;
           __syncwarp();
@@ -402,15 +409,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
       const uint32_t tempty0 = smem_u32(&sh.tmem_empty[0]), tfull0 = smem_u32(&sh.tmem_full[0]);
       uint32_t bi = 0, bp = 1;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < total_tiles && !*abort_flag; t += gridDim.x) {
+      for (int t = tile0; ok && t < total_tiles && !*abort_flag; t += tile_step) {
         const Tile8 tl = tile_of(t);
         // rows past the expert's last and columns past the last block: not stored, any scale does
         const float* xs0 = p.xs + static_cast<int64_t>(min(tl.row0 + i, tl.row_end - 1)) * p.xs_ld;
         const float* xs1 = p.xs + static_cast<int64_t>(min(tl.row0 + i + 64, tl.row_end - 1)) * p.xs_ld;
-        const float* ws0 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(tl.n0 >> 7) * p.ws_o;
-        const float* ws1 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(min(tl.n0 + C::kCols, p.O - 1) >> 7) * p.ws_o;
+        const float* ws0 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(tl.n0 >> 7) * p.ws_o +
+                           static_cast<int64_t>(kb0) * p.ws_c;
+        const float* ws1 = p.ws + tl.e * p.ws_e + static_cast<int64_t>(min(tl.n0 + C::kCols, p.O - 1) >> 7) * p.ws_o +
+                           static_cast<int64_t>(kb0) * p.ws_c;
 #pragma unroll 1
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           const float x0 = __ldg(xs0 + kb), x1 = __ldg(xs1 + kb);
           const float w0 = __ldg(ws0), w1 = __ldg(ws1);
           ws0 += p.ws_c;
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint32_t scale0 = smem_u32(&sh.scale[0][h][q * 32 + lane]);
     const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * C::kCols;
-    for (int t = blockIdx.x; t < total_tiles && !*abort_flag; t += gridDim.x) {
+    for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
       const Tile8 tl = tile_of(t);
       const int row = tl.row0 + q * 32 + lane;
       const int col0 = tl.n0 + h * C::kCols;
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
       if (!arrived()) goto promoted;   // aborted: nothing is stored
       tmem_ld_32x32b_x32_wait(trow + bi * BN, v[0]);
 #pragma unroll 1
-      for (int left = p.kblocks; left > 0; --left) {
+      for (int left = kb1 - kb0; left > 0; --left) {
         const uint32_t at = trow + bi * BN;
 #pragma unroll
         for (int c = 0; c + 1 < kChunks; ++c) tmem_ld_x32_fma(at + (c + 1) * 32, v[(c + 1) & 1], acc + c * 16, v[c & 1], s2);
@@ -484,7 +493,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int j = 0; j < 16; ++j) fma_f32x2(acc[(kChunks - 1) * 16 + j], v[1][2 * j], v[1][2 * j + 1], s);
         }
       }
-      if (valid) {
+      if (p.split > 1) {
+        // this part of the sum, [column][row] over the operand ring: every load into it has
+        // been multiplied, and a split CTA takes no further tile
+        float* part = reinterpret_cast<float*>(smem) + h * C::kCols * kRows8 + q * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < C::kCols / 2; ++j) {
+          part[(2 * j) * kRows8] = __uint_as_float(static_cast<uint32_t>(acc[j]));
+          part[(2 * j + 1) * kRows8] = __uint_as_float(static_cast<uint32_t>(acc[j] >> 32));
+        }
+      } else if (valid) {
         uint4* o4 = reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + col0);   // O % 8 == 0: 16-byte aligned
 #pragma unroll
         for (int j = 0; j < C::kCols / 8; ++j) {
@@ -497,6 +515,41 @@ __global__ void __launch_bounds__(kThreads8, 1)
       }
     }
   promoted:;
+  }
+
+  if (p.split > 1) {
+    // ---------------------------------------------------------------- join the parts
+    // Each CTA of the cluster adds the parts of its share of the tile's columns, in rank
+    // order, and writes them.  An aborted CTA's part is garbage, as the call's result is.
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8 && tile0 < total_tiles) {
+      const Tile8 tl = tile_of(tile0);
+      const int q = warp & 3, h = warp >> 2;
+      const int row = tl.row0 + q * 32 + lane;
+      const int share = BN / p.split;   // 32 columns at least: two warps of 16
+      for (int c = rank * share + h * (share / 2); c < rank * share + (h + 1) * (share / 2); c += 8) {
+        float sum[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+        const uint32_t at = smem_u32(smem) + (c * kRows8 + q * 32 + lane) * 4;
+        for (int r = 0; r < p.split; ++r) {
+          const uint32_t from = map_to_rank(at, r);
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = ld_shared_cluster_f32(from + j * kRows8 * 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(__float_as_uint(sum[2 * i]), __float_as_uint(sum[2 * i + 1]));
+        if (row < tl.row_end && tl.n0 + c < p.O)
+          *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + tl.n0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while another reads its part
   }
 
   // ---------------------------------------------------------------- teardown
@@ -582,9 +635,25 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) ready.fetch_or(uint64_t(1) << dev);
   }
+  // Tiles that leave more than half of the SMs without work are split over the contraction,
+  // as often as fits the SMs and leaves each part two k-blocks.
   const int64_t tiles = mt * p.num_nt;
-  const int grid = static_cast<int>(tiles < a.num_sms ? tiles : a.num_sms);
-  if (e == cudaSuccess) kern<<<grid, kThreads8, smem, a.stream>>>(tm_x, tm_w, p);
+  p.split = 1;
+  while (p.split < kMaxSplit && tiles * p.split * 2 <= a.num_sms && p.kblocks >= p.split * 4) p.split *= 2;
+  static_assert(BN * kRows8 * 4 <= C::kRing && BN / kMaxSplit % 16 == 0, "parts of a split");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads8);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? tiles * p.split : tiles < a.num_sms ? tiles : a.num_sms));
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);

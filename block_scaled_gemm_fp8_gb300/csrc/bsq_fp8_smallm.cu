@@ -70,22 +70,20 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp8_smallm_kernel(const Fp8S
     if (bad || r0 == r1) return;
   }
   const int n0 = blockIdx.x * kColsS;
-  const uint8_t* wrow[4];
+  // One pointer each for W and the tokens; a fragment's rows are 32-bit offsets from them
+  // (8 rows of W, 8 tokens apart).  Rows past N: any row, not stored.
+  const int rows_left = p.N - 1 - n0;
+  const uint8_t* wbase = p.w + (static_cast<int64_t>(e) * p.N + n0) * p.K + 16 * t;
+  uint32_t woff[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)   // rows past N: any row, not stored
-    wrow[i] = p.w + (static_cast<int64_t>(e) * p.N + min(n0 + 8 * i + g, p.N - 1)) * p.K + 16 * t;
+  for (int i = 0; i < 4; ++i) woff[i] = static_cast<uint32_t>(min(8 * i + g, rows_left)) * static_cast<uint32_t>(p.K);
   const float* ws = p.ws + (static_cast<int64_t>(e) * ((p.N + 127) >> 7) + (n0 >> 7)) * p.kblocks;
 
   for (int m0 = r0; m0 < r1; m0 += 8 * NT) {
-    const uint8_t* xrow[NT];
-    const float* xs[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {   // tokens past the last: any token, not stored
-      xrow[j] = p.x + static_cast<int64_t>(min(m0 + 8 * j + g, r1 - 1)) * p.K + 16 * t;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        xs[j][i] = p.xs + static_cast<int64_t>(min(m0 + 8 * j + 2 * t + i, r1 - 1)) * p.kblocks;
-    }
+    // tokens past the last: any token, not stored
+    const int last = r1 - 1 - m0;
+    const uint8_t* xbase = p.x + static_cast<int64_t>(m0) * p.K + 16 * t;
+    const float* sbase = p.xs + static_cast<int64_t>(m0) * p.kblocks;
     float acc[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -101,7 +99,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp8_smallm_kernel(const Fp8S
         const int k = kb * 128 + 64 * h;
         const bool in = k + 16 * t < p.K;   // K % 16 == 0: whole 16-byte pieces
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[h][i] = in ? ldg_stream(wrow[i] + k) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) v[h][i] = in ? ldg_stream(wbase + (woff[i] + k)) : make_uint4(0, 0, 0, 0);
       }
     };
     uint4 next[2][4];
@@ -125,10 +123,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp8_smallm_kernel(const Fp8S
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k = kb * 128 + 64 * h;
-          xv[j][h] = k + 16 * t < p.K ? __ldg(reinterpret_cast<const uint4*>(xrow[j] + k)) : make_uint4(0, 0, 0, 0);
+          const uint32_t off = static_cast<uint32_t>(min(8 * j + g, last)) * static_cast<uint32_t>(p.K) + k;
+          xv[j][h] = k + 16 * t < p.K ? __ldg(reinterpret_cast<const uint4*>(xbase + off)) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sx[j][i] = __ldg(xs[j][i] + kb);
+        for (int i = 0; i < 2; ++i) sx[j][i] = __ldg(sbase + (min(8 * j + 2 * t + i, last) * p.kblocks + kb));
       }
       if (AHEAD && kb + WARPS < p.kblocks) load_w(kb + WARPS, next);
 #pragma unroll
@@ -184,7 +183,15 @@ int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
 
 }  // namespace
 
-bool fp8_takes_smallm(const Fp8Args& a) { return !a.dgrad && (a.offsets ? a.S <= 4 * a.E : a.S <= 32); }
+// Up to 16 rows: one pass over W.  Up to 32: two, the second from L2, while W is small enough
+// to stay there beside what else runs (4096 x 4096, 32 rows: 11.2 us against 13.4 of the
+// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: batches of a few rows
+// each.  32-bit offsets within 32 rows bound K.
+bool fp8_takes_smallm(const Fp8Args& a) {
+  if (a.dgrad || a.K > (1 << 26)) return false;
+  if (a.offsets) return a.S <= 4 * a.E;
+  return a.S <= 16 || (a.S <= 32 && a.N * a.K <= (1 << 25));
+}
 
 int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
   Fp8SmallParams p;
@@ -200,13 +207,14 @@ int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
   p.K = static_cast<int32_t>(a.K);
   p.E = static_cast<int32_t>(a.E);
   p.kblocks = static_cast<int32_t>((a.K + 127) / 128);
-  // Dense: all rows in one pass, few CTAs, so many warps with a block in flight ahead.  Grouped:
-  // an expert of a decode batch rarely has more than 8 rows, and there are CTAs enough to
-  // fill every SM three times over, which keeps more bytes in flight than loading ahead.
-  if (a.offsets) return launch_typed<1, 8, false, 3>(p, a, msg);
-  if (a.S <= 8) return launch_typed<1, 16, true, 1>(p, a, msg);
-  if (a.S <= 16) return launch_typed<2, 16, true, 1>(p, a, msg);
-  return launch_typed<4, 8, false, 2>(p, a, msg);
+  // With CTAs enough to fill every SM several times over, small CTAs side by side keep more bytes
+  // in flight than one that loads ahead, and one's reduction hides behind another's loads
+  // (64 experts of 2816 x 2048, 64 rows: 36 us against 61).
+  // With fewer, one CTA of 16 warps an SM (4096 x 4096: 5.8 us for 8 rows, 7.2 for 16).  An
+  // expert of a decode batch rarely has more than 8 rows.
+  const bool many = a.offsets || (a.N + kColsS - 1) / kColsS >= 2 * a.num_sms;
+  if (a.offsets || a.S <= 8) return many ? launch_typed<1, 8, false, 3>(p, a, msg) : launch_typed<1, 16, true, 1>(p, a, msg);
+  return many ? launch_typed<2, 8, false, 2>(p, a, msg) : launch_typed<2, 16, false, 1>(p, a, msg);
 }
 
 }  // namespace bsq

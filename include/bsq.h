@@ -294,7 +294,7 @@ bsq_status bsq_quantize_e4m3(int32_t dtype, const void* x, int64_t batch, int64_
  * x_codes: u8[M][K], x_scale: f32[M][ceil(K/128)] (bsq_quantize_e4m3, block_rows 1);
  * W: [N][K] in w_fmt, which must be BSQ_FP8_E4M3_B128.  K % 16 == 0, N % 8 == 0; codes, W's
  * scales and y 16-byte aligned, x_scale 4-byte.  y: bf16[M][N], fully written; K == 0 gives zeros.
- * M <= 32 takes a kernel that streams W once for all its rows.
+ * A few rows (M <= 16, or 32 with a small W) take a kernel that streams W into registers.
  */
 bsq_status bsq_fp8_forward(const void* x_codes, const float* x_scale, int64_t M, int32_t w_fmt, const void* w_data,
                            const float* w_scale, int64_t N, int64_t K, void* y, void* stream);
