@@ -13,12 +13,13 @@
 // r above zero keeps at least the smallest code above zero, so that a later step does not
 // divide a remembered m by eps alone.
 //
-// Every operation is rounded by itself (no contraction), so the step equals the same
-// formula in float32 tensor operations bit for bit.
+// Every operation of the states is rounded by itself (no contraction), so that the codes
+// follow from the formula; the update's quotient, which no state sees, is within 2 ulp.
 //
-// Bound by HBM: 28 or 30 bytes per element with 32-bit states and a BF16 copy (14.1 to 16.1
-// with 8-bit ones).  A thread owns 8 consecutive elements (32-byte accesses), 16 lanes a
-// scale block, a CTA a chunk of one tensor, found by bisection in the launch's table.
+// Bound by HBM: 28 or 30 bytes per element with 32-bit states and a BF16 copy; 16.1 or 18.1
+// with 8-bit ones, where the instructions of the rounding weigh as much.  A thread owns 8
+// consecutive elements (32-byte accesses), 16 lanes a scale block, a CTA a chunk of one
+// tensor, found by bisection in the launch's table.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -32,9 +33,15 @@ namespace {
 
 constexpr int kThreadsA = 256;
 constexpr int kStepA = kThreadsA * 8;      // elements of one sweep of a CTA
-constexpr int kSweeps = 2;
-constexpr int kChunkA = kStepA * kSweeps;
-constexpr int kTableA = 256;               // tensors of one launch
+// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (146 M elements: 470
+// us, 5.0 TB/s; 541 of one sweep); with 32-bit ones, where instructions do not count, one
+// (300 small tensors, 5.7 M elements: 29.5 us against 37.3 of two).  Loading a sweep ahead in
+// registers changed nothing (472 us).
+template <bool S8>
+constexpr int kSweeps = S8 ? 8 : 1;
+// Tensors of one launch: the table travels as a kernel parameter, so there are a small one
+// (2.4 KB) and the largest that fits the 32764 bytes of parameters.
+constexpr int kFewA = 32, kManyA = 400;
 
 struct AdamwEntry {
   float* p;
@@ -51,15 +58,16 @@ struct AdamwEntry {
   int32_t wide;          // every pointer allows the vector accesses
 };
 
+template <int N>
 struct AdamwTable {
-  AdamwEntry e[kTableA];
+  AdamwEntry e[N];
   int32_t count;
   float b1, c1m, b2, c2m;   // betas and 1 - betas
   float lr1, rc2, eps;      // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t salt;            // seed and step
   const float* grad_scale;
 };
-static_assert(sizeof(AdamwTable) <= 32764, "kernel parameter space");
+static_assert(sizeof(AdamwTable<kManyA>) <= 32764, "kernel parameter space");
 
 __device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
   asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -93,6 +101,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return f;
 }
 
+// 1 / x within 1 ulp; an x below 2^-126 counts as zero.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // 32 random bits of an element: a Weyl step and MurmurHash3's finalizer (Appleby).
 __device__ __forceinline__ uint32_t element_bits(uint32_t i, uint32_t salt) {
   uint32_t x = i * 0x9E3779B1u + salt;
@@ -101,15 +116,18 @@ __device__ __forceinline__ uint32_t element_bits(uint32_t i, uint32_t salt) {
   return x ^ (x >> 16);
 }
 
-// E4M3 magnitude next to a (0 <= a, about 448 at most), up with the probability of the part
-// cut off: 16 random bits against the mantissa bits below E4M3's three, or against the
-// part below its subnormal step of 2^-9.  NaN stays.
-__device__ __forceinline__ float round_at_random(float a, uint32_t bits) {
-  const float big = __uint_as_float((__float_as_uint(a) + (bits << 4)) & 0xFFF00000u);
-  const float small = __fmul_rn(floorf(__fadd_rn(__fmul_rn(a, 512.f), __fmul_rn(static_cast<float>(bits), 1.52587890625e-5f))),
-                                1.953125e-3f);
-  const float r = a >= 0.015625f ? big : small;
-  return r > 448.f ? 448.f : r;
+// E4M3 magnitude next to a, up with the probability of the part cut off: 16 random bits
+// against the mantissa bits below E4M3's three.  For 2^-6 <= a <= 448 and a little above.
+__device__ __forceinline__ float round_normal(float a, uint32_t bits) {
+  return fminf(__uint_as_float((__float_as_uint(a) + (bits << 4)) & 0xFFF00000u), 448.f);
+}
+// The same for every a >= 0 (NaN stays): below 2^-6, against the part below the subnormal
+// step of 2^-9.  x + 2^23 rounded down, less 2^23, is the floor of an x below 2^22.
+__device__ __forceinline__ float round_any(float a, uint32_t bits) {
+  if (a >= 0.015625f) return round_normal(a, bits);
+  const float u = __uint_as_float(0x43000000u | bits) - 128.f;   // bits / 65536
+  const float x = __fadd_rn(__fmul_rn(a, 512.f), u);
+  return __fmul_rn(__fadd_rd(x, 8388608.f) - 8388608.f, 1.953125e-3f);
 }
 
 __device__ __forceinline__ float block_amax(float a) {
@@ -127,8 +145,8 @@ __device__ __forceinline__ float lane16_amax(const float (&x)[8]) {
   return block_amax(__uint_as_float(m));
 }
 
-template <bool G16, bool S8>
-__global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant__ AdamwTable t) {
+template <bool G16, bool S8, int N>
+__global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_constant__ AdamwTable<N> t) {
   int lo = 0, hi = t.count - 1;
   const int chunk = blockIdx.x;
   while (lo < hi) {
@@ -138,14 +156,14 @@ __global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant_
   }
   const AdamwEntry& e = t.e[lo];
   const float gs = t.grad_scale ? __ldg(t.grad_scale) : 1.f;
-  const int64_t first = static_cast<int64_t>(chunk - e.chunk0) * kChunkA + threadIdx.x * 8;
-#pragma unroll
-  for (int sweep = 0; sweep < kSweeps; ++sweep) {
+  const int64_t first = static_cast<int64_t>(chunk - e.chunk0) * (kSweeps<S8> * kStepA) + threadIdx.x * 8;
+#pragma unroll 1
+  for (int sweep = 0; sweep < kSweeps<S8>; ++sweep) {
     const int64_t i0 = first + sweep * kStepA;
     const int64_t left = e.n - i0;
     const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;   // elements of this thread
     const bool wide = e.wide && n == 8;
-    if (!S8 && n == 0) continue;
+    if (!S8 && n == 0) return;
     float g[8], p[8], m[8], v[8];
     float ms = 0.f, vs = 0.f;
     if (S8 && n > 0) {
@@ -200,46 +218,78 @@ __global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant_
       }
     }
     float r[8];
+    // two elements an instruction: each operation still rounded by itself
+    auto two = [](float x) { return make_float2(x, x); };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float gj = __fmul_rn(g[j], gs);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 gj = __fmul2_rn(make_float2(g[j], g[j + 1]), two(gs));
+      float2 mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]);
       if (S8) {
-        m[j] = __fmul_rn(m[j], ms);
-        v[j] = __fmul_rn(v[j], vs);
-        v[j] = __fmul_rn(v[j], v[j]);
+        mj = __fmul2_rn(mj, two(ms));
+        vj = __fmul2_rn(vj, two(vs));
+        vj = __fmul2_rn(vj, vj);
       }
-      m[j] = __fadd_rn(__fmul_rn(m[j], t.b1), __fmul_rn(gj, t.c1m));
-      v[j] = __fadd_rn(__fmul_rn(v[j], t.b2), __fmul_rn(__fmul_rn(gj, gj), t.c2m));
-      r[j] = __fsqrt_rn(v[j]);
-      const float u = __fdiv_rn(__fmul_rn(m[j], t.lr1), __fadd_rn(__fmul_rn(r[j], t.rc2), t.eps));
-      p[j] = __fsub_rn(__fmul_rn(p[j], e.decay), u);
-      if (S8 && j >= n) m[j] = r[j] = 0.f;   // past the end: no part of the block's maximum
+      mj = __fadd2_rn(__fmul2_rn(mj, two(t.b1)), __fmul2_rn(gj, two(t.c1m)));
+      vj = __fadd2_rn(__fmul2_rn(vj, two(t.b2)), __fmul2_rn(__fmul2_rn(gj, gj), two(t.c2m)));
+      const float2 rj = make_float2(__fsqrt_rn(vj.x), __fsqrt_rn(vj.y));
+      const float2 den = __fadd2_rn(__fmul2_rn(rj, two(t.rc2)), two(t.eps));
+      const float2 u = __fmul2_rn(__fmul2_rn(mj, two(t.lr1)), make_float2(reciprocal(den.x), reciprocal(den.y)));
+      const float2 pj = __fadd2_rn(__fmul2_rn(make_float2(p[j], p[j + 1]), two(e.decay)), make_float2(-u.x, -u.y));
+      p[j] = pj.x, p[j + 1] = pj.y;
+      m[j] = mj.x, m[j + 1] = mj.y;
+      v[j] = vj.x, v[j + 1] = vj.y;
+      r[j] = rj.x, r[j + 1] = rj.y;
     }
-    uint32_t cm[8], cv[8];
+    if (S8 && n < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= n) m[j] = r[j] = 0.f;   // past the end: no part of the block's maximum
+    }
+    uint32_t cm[4], cv[4];   // codes, two a word
     if (S8) {
+      // One division each for 448 / a and a / 448 of both states: m's by the lower half of the
+      // block's 16 lanes, r's by the upper.
+      const int lane = threadIdx.x & 31;
+      const bool upper = (lane & 8) != 0;
       const float am = lane16_amax(m), ar = lane16_amax(r);
-      const float im = __fdiv_rn(448.f, am), ir = __fdiv_rn(448.f, ar);
-      if (n > 0 && (threadIdx.x & 15) == 0) {
-        e.ms[i0 >> 7] = __fdiv_rn(am, 448.f);
-        e.vs[i0 >> 7] = __fdiv_rn(ar, 448.f);
-      }
+      const float a = upper ? ar : am;
+      const float inv = __fdiv_rn(448.f, a);
+      const float im = __shfl_sync(0xffffffffu, inv, lane & 16), ir = __shfl_sync(0xffffffffu, inv, (lane & 16) | 8);
+      const float scale = __fdiv_rn(a, 448.f);
+      // lane 0 of the block has its first element; lane 8 may be past the tensor's end
+      const int64_t block = (i0 - (upper ? 64 : 0)) >> 7;
+      if ((lane & 7) == 0 && (block << 7) < e.n) (upper ? e.vs : e.ms)[block] = scale;
       const uint32_t at = e.counter + static_cast<uint32_t>(i0);
+      float qm[8], qr[8];
+      float least = 1.f;
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        float qm[2], qv[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t bits = element_bits(at + j + k, t.salt);
-          const float xm = __fmul_rn(m[j + k], im), xr = __fmul_rn(r[j + k], ir);
-          qm[k] = copysignf(round_at_random(fabsf(xm), bits & 0xFFFFu), xm);
-          const float q = round_at_random(xr, bits >> 16);
-          qv[k] = xr > 0.f && q == 0.f ? 1.953125e-3f : q;
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = element_bits(at + j, t.salt);
+        if ((j & 1) == 0) {
+          const float2 mj = __fmul2_rn(make_float2(m[j], m[j + 1]), two(im)), rj = __fmul2_rn(make_float2(r[j], r[j + 1]), two(ir));
+          m[j] = mj.x, m[j + 1] = mj.y;
+          r[j] = rj.x, r[j + 1] = rj.y;
         }
-        const uint32_t c2m = e4m3x2(qm[0], qm[1]), c2v = e4m3x2(qv[0], qv[1]);
-        cm[j] = c2m & 0xFFu;
-        cm[j + 1] = c2m >> 8;
-        cv[j] = c2v & 0xFFu;
-        cv[j + 1] = c2v >> 8;
+        const float am_j = fabsf(m[j]);
+        least = fminf(least, fminf(am_j, r[j]));
+        qm[j] = copysignf(round_normal(am_j, bits & 0xFFFFu), m[j]);
+        qr[j] = round_normal(r[j], bits >> 16);
+      }
+      // Below 2^-6 (2^-15 of the block's largest: rare), or NaN, which only a NaN or infinite
+      // scale leaves: once more in full.
+      if (!(least >= 0.015625f) || !(inv > 0.f)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t bits = element_bits(at + j, t.salt);
+          qm[j] = copysignf(round_any(fabsf(m[j]), bits & 0xFFFFu), m[j]);
+          const float q = round_any(r[j], bits >> 16);
+          qr[j] = r[j] > 0.f && q == 0.f ? 1.953125e-3f : q;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cm[j] = e4m3x2(qm[2 * j], qm[2 * j + 1]);
+        cv[j] = e4m3x2(qr[2 * j], qr[2 * j + 1]);
       }
     }
     if (wide) {
@@ -253,9 +303,8 @@ __global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant_
         *reinterpret_cast<uint4*>(e.copy + i0) = w;
       }
       if (S8) {
-        auto four = [](const uint32_t* c) { return c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24); };
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + i0) = make_uint2(four(cm), four(cm + 4));
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + i0) = make_uint2(four(cv), four(cv + 4));
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + i0) = make_uint2(cm[0] | (cm[1] << 16), cm[2] | (cm[3] << 16));
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + i0) = make_uint2(cv[0] | (cv[1] << 16), cv[2] | (cv[3] << 16));
       } else {
         st8(static_cast<float*>(e.m) + i0, m);
         st8(static_cast<float*>(e.v) + i0, v);
@@ -267,8 +316,8 @@ __global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant_
           e.p[i0 + j] = p[j];
           if (e.copy) e.copy[i0 + j] = __float2bfloat16_rn(p[j]);
           if (S8) {
-            static_cast<uint8_t*>(e.m)[i0 + j] = static_cast<uint8_t>(cm[j]);
-            static_cast<uint8_t*>(e.v)[i0 + j] = static_cast<uint8_t>(cv[j]);
+            static_cast<uint8_t*>(e.m)[i0 + j] = static_cast<uint8_t>(cm[j >> 1] >> (8 * (j & 1)));
+            static_cast<uint8_t*>(e.v)[i0 + j] = static_cast<uint8_t>(cv[j >> 1] >> (8 * (j & 1)));
           } else {
             static_cast<float*>(e.m)[i0 + j] = m[j];
             static_cast<float*>(e.v)[i0 + j] = v[j];
@@ -281,12 +330,11 @@ __global__ void __launch_bounds__(kThreadsA) adamw_kernel(const __grid_constant_
 
 bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-}  // namespace
-
-int launch_adamw(const AdamwArgs& a, const char** msg) {
+template <int N>
+int launch_tables(const AdamwArgs& a, const char** msg) {
   const bsq_adamw_tensor* ts = static_cast<const bsq_adamw_tensor*>(a.tensors);
   const bool g16 = a.grad_dtype == BSQ_DT_BF16, s8 = a.state_bits == 8;
-  AdamwTable t;
+  AdamwTable<N> t;
   t.b1 = static_cast<float>(a.beta1);
   t.c1m = static_cast<float>(1.0 - a.beta1);
   t.b2 = static_cast<float>(a.beta2);
@@ -300,14 +348,11 @@ int launch_adamw(const AdamwArgs& a, const char** msg) {
   while (i < a.count) {
     t.count = 0;
     int64_t chunks = 0;
-    for (; i < a.count && t.count < kTableA; ++i) {
+    for (; i < a.count && t.count < N; ++i) {
       const bsq_adamw_tensor& s = ts[i];
       if (s.n == 0) continue;
-      const int64_t c = (s.n + kChunkA - 1) / kChunkA;
-      if (c > INT32_MAX) {
-        *msg = "a tensor is too long";
-        return -1;
-      }
+      const int64_t chunk = static_cast<int64_t>(s8 ? kSweeps<true> : kSweeps<false>) * kStepA;
+      const int64_t c = (s.n + chunk - 1) / chunk;
       if (chunks + c > INT32_MAX) break;   // the next launch takes it
       AdamwEntry& e = t.e[t.count++];
       e.p = static_cast<float*>(s.param);
@@ -326,10 +371,10 @@ int launch_adamw(const AdamwArgs& a, const char** msg) {
     }
     if (t.count == 0) break;
     const dim3 grid(static_cast<unsigned>(chunks));
-    if (g16 && s8) adamw_kernel<true, true><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else if (g16) adamw_kernel<true, false><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else if (s8) adamw_kernel<false, true><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else adamw_kernel<false, false><<<grid, kThreadsA, 0, a.stream>>>(t);
+    if (g16 && s8) adamw_kernel<true, true, N><<<grid, kThreadsA, 0, a.stream>>>(t);
+    else if (g16) adamw_kernel<true, false, N><<<grid, kThreadsA, 0, a.stream>>>(t);
+    else if (s8) adamw_kernel<false, true, N><<<grid, kThreadsA, 0, a.stream>>>(t);
+    else adamw_kernel<false, false, N><<<grid, kThreadsA, 0, a.stream>>>(t);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
       *msg = cudaGetErrorString(e);
@@ -337,6 +382,12 @@ int launch_adamw(const AdamwArgs& a, const char** msg) {
     }
   }
   return 0;
+}
+
+}  // namespace
+
+int launch_adamw(const AdamwArgs& a, const char** msg) {
+  return a.count <= kFewA ? launch_tables<kFewA>(a, msg) : launch_tables<kManyA>(a, msg);
 }
 
 }  // namespace bsq

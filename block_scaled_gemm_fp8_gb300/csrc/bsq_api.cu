@@ -569,7 +569,7 @@ bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, int32_t gra
         (reinterpret_cast<uintptr_t>(t.copy) & 1u))
       return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: a pointer is not aligned to its elements", what, i);
     if (!std::isfinite(t.weight_decay)) return fail(BSQ_ERR_INVALID_ARG, "%s: tensor %d: weight_decay not finite", what, i);
-    if (t.n > (static_cast<int64_t>(1) << 40)) return fail(BSQ_ERR_UNSUPPORTED, "%s: tensor %d: above 2^40 elements", what, i);
+    if (t.n > (static_cast<int64_t>(1) << 40)) return fail(BSQ_ERR_UNSUPPORTED, "%s: tensor %d: above 2^40 elements", what, i);   // one launch's grid
     total += t.n;
   }
   if (total == 0) return BSQ_OK;

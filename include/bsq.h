@@ -336,11 +336,11 @@ typedef struct {
 } bsq_adamw_tensor;
 
 /*
- * bsq_adamw -- one AdamW step over many tensors (one launch per 256):
+ * bsq_adamw -- one AdamW step over many tensors (one launch per 400):
  *     g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *     param = param (1 - lr weight_decay)
  *             - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in float32, each operation rounded by itself.  state_bits 8: m and sqrt(v) are kept as
+ * in float32, each operation rounded by itself (the quotient within 2 ulp).  state_bits 8: m and sqrt(v) are kept as
  * E4M3 codes with a scale per 128 elements (bsq_quantize_e4m3's rule), the new codes rounded
  * at random from a hash of (seed + step * 0x7F4A7C15, counter + index): the same arguments
  * give the same codes.  A sqrt(v) above zero keeps at least the smallest code above zero.
