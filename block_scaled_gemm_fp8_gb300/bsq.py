@@ -303,31 +303,31 @@ def quantize_e4m3(x, block_rows=1, codes=None, scale=None, stream=None):
 
 def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
     wd, ws, batch, n, k = w.data, w.scale, w.batch, w.rows, w.cols
-    _dense(codes, _CODES, name)
-    _dense(scale, _F32, name)
-    _dense(wd, _CODES, name)
-    _dense(ws, _F32, name)
-    if not codes.get_device() == scale.get_device() == wd.get_device() == ws.get_device():
-        raise ValueError(f"{name}: operands on different devices")
-    rows, blocks = codes.shape[0], (inner + 127) // 128
-    if codes.shape != (rows, inner) or scale.shape != (rows, blocks):
-        raise ValueError(f"{name}: codes {tuple(codes.shape)} with scale {tuple(scale.shape)}; [rows, {inner}] with "
-                         f"[rows, {blocks}] are wanted")
-    if wd.numel() != batch * n * k or (w.fmt == BSQ_FP8_E4M3_B128 and
-                                       ws.numel() != batch * ((n + 127) // 128) * ((k + 127) // 128)):
-        raise ValueError(f"{name}: w holds {wd.numel()} codes and {ws.numel()} scales for [{batch}, {n}, {k}]")
+    dev, rows, blocks = codes.get_device(), codes.shape[0], (inner + 127) // 128
+    # one expression for the common case; what is wrong is looked for only when it fails
+    if not (dev >= 0 and scale.get_device() == wd.get_device() == ws.get_device() == dev and codes.dtype in _CODES
+            and wd.dtype in _CODES and scale.dtype is torch.float32 and ws.dtype is torch.float32
+            and codes.shape == (rows, inner) and scale.shape == (rows, blocks) and codes.is_contiguous()
+            and scale.is_contiguous() and wd.is_contiguous() and ws.is_contiguous() and wd.numel() == batch * n * k
+            and (w.fmt != BSQ_FP8_E4M3_B128 or ws.numel() == batch * ((n + 127) // 128) * ((k + 127) // 128))):
+        for t, dtypes, what in ((codes, _CODES, "codes"), (scale, _F32, "scale"), (wd, _CODES, "w.data"), (ws, _F32, "w.scale")):
+            _dense(t, dtypes, f"{name}: {what}")
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} on {codes.device}, scale {tuple(scale.shape)} on {scale.device}; "
+                         f"[rows, {inner}] and [rows, {blocks}] are wanted; w holds {wd.numel()} codes and {ws.numel()} scales "
+                         f"on {wd.device} and {ws.device} for [{batch}, {n}, {k}]")
     out = _out(out, (rows, outer), torch.bfloat16, codes, stream, name)
+    fn = getattr(_lib or lib(), "bsq_" + name)
+    raw = _raw_stream(stream, codes)
     if offsets is None:
         if batch != 1:
             raise ValueError(f"{name}: one weight is wanted, not {batch}")
-        _check(getattr(lib(), "bsq_" + name)(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(),
-                                             n, k, out.data_ptr(), _raw_stream(stream, codes)))
+        _check(fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), n, k, out.data_ptr(), raw))
     else:
         _dense(offsets, (torch.int32,), name)
-        if offsets.numel() != batch:
-            raise ValueError(f"{name}: {offsets.numel()} offsets for {batch} experts")
-        _check(getattr(lib(), "bsq_" + name)(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(),
-                                             batch, n, k, offsets.data_ptr(), out.data_ptr(), _raw_stream(stream, codes)))
+        if offsets.numel() != batch or offsets.get_device() != dev:
+            raise ValueError(f"{name}: {offsets.numel()} offsets on {offsets.device} for {batch} experts")
+        _check(fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), batch, n, k,
+                  offsets.data_ptr(), out.data_ptr(), raw))
     return out
 
 

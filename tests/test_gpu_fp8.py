@@ -72,7 +72,8 @@ def check(out, ref, a, b, kc, what):
 
 
 DENSE = [(1, 8, 16), (1, 128, 128), (3, 40, 144), (8, 256, 512), (9, 1000, 400), (16, 264, 2064), (17, 520, 1024),
-         (32, 128, 4096), (33, 256, 128), (64, 8, 640), (129, 264, 96), (256, 256, 1024), (257, 776, 1168), (600, 1320, 2064)]
+         (32, 128, 4096), (33, 256, 128), (64, 8, 640), (129, 264, 96), (256, 256, 1024), (257, 776, 1168), (600, 1320, 2064),
+         (100, 1024, 5136), (40, 136, 4112)]   # the last two: tiles split over a cluster, uneven parts
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -87,7 +88,7 @@ def test_forward(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 128, 128), (5, 144, 48), (16, 2064, 272), (129, 96, 256), (256, 512, 512),
-                                   (300, 1168, 784), (520, 256, 2064)])
+                                   (300, 1168, 784), (520, 256, 2064), (70, 4112, 528)])
 def test_dgrad(M, N, K):
     gc, gs = draw_rows(M, N, 3)
     wc, ws = draw_weight(1, N, K, 4)
