@@ -24,7 +24,7 @@
 
 #include <cuda_bf16.h>
 
-#include "bsq_internal.h"
+#include "bsq_fp8_internal.h"
 #include "../../include/bsq.h"
 
 namespace bsq {

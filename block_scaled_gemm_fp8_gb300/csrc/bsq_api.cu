@@ -9,6 +9,7 @@
 
 #include <cuda_runtime.h>
 
+#include "bsq_fp8_internal.h"
 #include "bsq_internal.h"
 #include "../../include/bsq.h"
 

@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include "bsq_fp8_internal.h"
 #include "bsq_internal.h"
 #include "bsq_pipe.cuh"
 #include "bsq_ptx.cuh"

@@ -11,7 +11,7 @@
 // added in warp order through shared memory, so results do not depend on timing.
 #include <cuda_bf16.h>
 
-#include "bsq_internal.h"
+#include "bsq_fp8_internal.h"
 #include "../../include/bsq.h"
 
 namespace bsq {

@@ -10,7 +10,7 @@
 // infinite and its own code NaN.
 #include <cuda_bf16.h>
 
-#include "bsq_internal.h"
+#include "bsq_fp8_internal.h"
 #include "../../include/bsq.h"
 
 namespace bsq {
