@@ -58,6 +58,8 @@ constexpr int kTmemCols8 = 512;
 constexpr int kPromoteWarps = 8, kScaleWarps = 2;
 constexpr int kMaxStages8 = 6;
 constexpr int kMaxBufs8 = 4;
+constexpr int kStagePitch = 80;             // output staging of a warp: 32 rows of 64 bytes, 16 apart: no bank conflicts
+constexpr int kOutBytes = kPromoteWarps * 32 * kStagePitch;
 constexpr int kMaxSplit = 4;                // clusters of 8 do not all fit the SMs at once
 
 // BN: output columns of a tile.  MN: W is contracted over its rows (dgrad).
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   using C = Fp8Cfg<BN, MN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing);
+  Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing + kOutBytes);
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same in every lane
@@ -448,13 +450,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
     static_assert(kChunks % 2 == 0, "register double buffer");
     uint32_t bi = 0, bp = 0;   // TMEM buffer and its parity
     const uint32_t scale0 = smem_u32(&sh.scale[0][h][q * 32 + lane]);
+    const uint32_t stage = smem_u32(smem + C::kRing) + warp * (32 * kStagePitch);
     const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * C::kCols;
     for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
       const Tile8 tl = tile_of(t);
-      const int row = tl.row0 + q * 32 + lane;
       const int col0 = tl.n0 + h * C::kCols;
-      const bool valid = row < tl.row_end;
       uint64_t acc[C::kCols / 2];
 #pragma unroll
       for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
@@ -503,15 +504,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
           part[(2 * j) * kRows8] = __uint_as_float(static_cast<uint32_t>(acc[j]));
           part[(2 * j + 1) * kRows8] = __uint_as_float(static_cast<uint32_t>(acc[j] >> 32));
         }
-      } else if (valid) {
-        uint4* o4 = reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + col0);   // O % 8 == 0: 16-byte aligned
+      } else {
+        // 32 columns at a time through shared memory, so that a store instruction writes 64
+        // bytes of 8 rows instead of 16 bytes of 32
 #pragma unroll
-        for (int j = 0; j < C::kCols / 8; ++j) {
-          uint32_t w[4];
+        for (int c = 0; c < C::kCols / 32; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack_bf16x2(static_cast<uint32_t>(acc[4 * j + i]), static_cast<uint32_t>(acc[4 * j + i] >> 32));
-          if (col0 + 8 * j < p.O) o4[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int j = 0; j < 16; ++j)
+            w[j] = pack_bf16x2(static_cast<uint32_t>(acc[c * 16 + j]), static_cast<uint32_t>(acc[c * 16 + j] >> 32));
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sts128(stage + lane * kStagePitch + 16 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + (lane >> 2);
+            const uint4 o = lds128(stage + r * kStagePitch + 16 * (lane & 3));
+            const int row = tl.row0 + q * 32 + r, col = col0 + c * 32 + 8 * (lane & 3);
+            if (row < tl.row_end && col < p.O)   // O % 8 == 0: whole 16-byte pieces
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + col) = o;
+          }
         }
       }
     }
@@ -617,8 +630,8 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     *msg = "too many output tiles";
     return -1;
   }
-  static_assert(C::kRing + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
-  const size_t smem = static_cast<size_t>(C::kRing) + sizeof(Fp8Shared) + 1024;
+  static_assert(C::kRing + kOutBytes + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
+  const size_t smem = static_cast<size_t>(C::kRing) + kOutBytes + sizeof(Fp8Shared) + 1024;
   auto kern = bsq_fp8_kernel<BN, MN>;
   static std::atomic<uint64_t> ready;   // devices (one bit each) on which the kernel is set up
   int dev = 0;
@@ -636,11 +649,14 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) ready.fetch_or(uint64_t(1) << dev);
   }
-  // Tiles that leave more than half of the SMs without work are split over the contraction,
-  // as often as fits the SMs and leaves each part two k-blocks.
+  // Tiles that leave more than half of the SMs without work are split over the contraction, as
+  // often as fits the SMs, if it is long enough: joining the parts takes about 3 us, a k-block
+  // 0.4 to 0.5 (128 x 512 x 7168, 56 k-blocks: 29 us whole, 15 in four; 8 k-blocks: 9.0 whole,
+  // 9.9 in two).
   const int64_t tiles = mt * p.num_nt;
   p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split * 2 <= a.num_sms && p.kblocks >= p.split * 4) p.split *= 2;
+  if (p.kblocks >= 12)
+    while (p.split < kMaxSplit && tiles * p.split * 2 <= a.num_sms && p.kblocks >= p.split * 8) p.split *= 2;
   static_assert(BN * kRows8 * 4 <= C::kRing && BN / kMaxSplit % 16 == 0, "parts of a split");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
