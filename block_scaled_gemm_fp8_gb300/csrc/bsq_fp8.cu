@@ -58,8 +58,7 @@ constexpr int kTmemCols8 = 512;
 constexpr int kPromoteWarps = 8, kScaleWarps = 2;
 constexpr int kMaxStages8 = 6;
 constexpr int kMaxBufs8 = 4;
-constexpr int kStagePitch = 80;             // output staging of a warp: 32 rows of 64 bytes, 16 apart: no bank conflicts
-constexpr int kOutBytes = kPromoteWarps * 32 * kStagePitch;
+constexpr int kBoxBytes8 = 32 * 128;        // output box: 32 rows of 64 columns
 constexpr int kMaxSplit = 4;                // clusters of 8 do not all fit the SMs at once
 
 // BN: output columns of a tile.  MN: W is contracted over its rows (dgrad).
@@ -67,10 +66,12 @@ template <int BN, bool MN>
 struct Fp8Cfg {
   static constexpr int kBBytes = BN * kDepth;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = BN == 256 ? 3 : 4;
   static constexpr int kBufs = kTmemCols8 / BN;         // accumulators in TMEM
   static constexpr int kCols = BN / 2;                  // output columns of one promotion warp
   static constexpr int kRing = kStages * kStage;
+  static constexpr int kOutWarp = kCols / 64 * kBoxBytes8;   // output staging of one promotion warp
+  static constexpr int kOutBytes = kPromoteWarps * kOutWarp;
 };
 
 struct Fp8Params {
@@ -245,6 +246,11 @@ __device__ __forceinline__ void tmem_ld_x32_fma(uint32_t taddr, uint32_t (&next)
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+
 // One tile: the expert and its rows, and the first output column.
 struct Tile8 {
   int e, row0, row_end, n0;
@@ -252,11 +258,12 @@ struct Tile8 {
 
 template <int BN, bool MN>
 __global__ void __launch_bounds__(kThreads8, 1)
-    bsq_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Fp8Params p) {
+    bsq_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_y, const Fp8Params p) {
   using C = Fp8Cfg<BN, MN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing + kOutBytes);
+  Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing + C::kOutBytes);
   volatile uint32_t* abort_flag = &sh.abort_flag;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same in every lane
@@ -450,7 +457,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     static_assert(kChunks % 2 == 0, "register double buffer");
     uint32_t bi = 0, bp = 0;   // TMEM buffer and its parity
     const uint32_t scale0 = smem_u32(&sh.scale[0][h][q * 32 + lane]);
-    const uint32_t stage = smem_u32(smem + C::kRing) + warp * (32 * kStagePitch);
+    const uint32_t stage = smem_u32(smem + C::kRing) + warp * C::kOutWarp;
     const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * C::kCols;
     for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
@@ -505,30 +512,44 @@ __global__ void __launch_bounds__(kThreads8, 1)
           part[(2 * j + 1) * kRows8] = __uint_as_float(static_cast<uint32_t>(acc[j] >> 32));
         }
       } else {
-        // 32 columns at a time through shared memory, so that a store instruction writes 64
-        // bytes of 8 rows instead of 16 bytes of 32
+        // The warp's 32 rows x kCols columns go through shared memory (64-column boxes, 128-byte
+        // swizzled) and from there by TMA, which writes them while the next tile is multiplied.
+        if (lane == 0) bulk_wait_read0();   // the last tile's have been read
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) {
-          uint32_t w[16];
+        for (int c = 0; c < C::kCols / 8; ++c) {
+          uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = pack_bf16x2(static_cast<uint32_t>(acc[c * 16 + j]), static_cast<uint32_t>(acc[c * 16 + j] >> 32));
+          for (int j = 0; j < 4; ++j)
+            w[j] = pack_bf16x2(static_cast<uint32_t>(acc[4 * c + j]), static_cast<uint32_t>(acc[4 * c + j] >> 32));
+          sts128(stage + (c / 8) * kBoxBytes8 + lane * 128 + (((c % 8) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
+        const int row0 = tl.row0 + q * 32;
+        if (row0 + 32 <= tl.row_end || !p.offsets) {
+          // rows past S and columns past O are clipped
+          fence_proxy_async_smem();
           __syncwarp();
+          if (lane == 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sts128(stage + lane * kStagePitch + 16 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            for (int c = 0; c < C::kCols; c += 64)
+              if (row0 < p.S && col0 + c < p.O) tma_store_2d(&tm_y, stage + (c / 64) * kBoxBytes8, col0 + c, row0);
+            bulk_commit();
+          }
+        } else {
+          // the next expert's rows begin within these 32: plain stores of this one's
           __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + (lane >> 2);
-            const uint4 o = lds128(stage + r * kStagePitch + 16 * (lane & 3));
-            const int row = tl.row0 + q * 32 + r, col = col0 + c * 32 + 8 * (lane & 3);
-            if (row < tl.row_end && col < p.O)   // O % 8 == 0: whole 16-byte pieces
-              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.O + col) = o;
+#pragma unroll 4
+          for (int i = lane; i < 32 * (C::kCols / 8); i += 32) {
+            const int r = i / (C::kCols / 8), c = i % (C::kCols / 8);
+            const uint4 o = lds128(stage + (c / 8) * kBoxBytes8 + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+            if (row0 + r < tl.row_end && col0 + 8 * c < p.O)   // O % 8 == 0: whole 16-byte pieces
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row0 + r) * p.O + col0 + 8 * c) = o;
           }
         }
       }
     }
-  promoted:;
+  promoted:
+    if (lane == 0) bulk_wait_all0();   // this warp's stores have been performed
   }
 
   if (p.split > 1) {
@@ -585,7 +606,7 @@ template <int BN, bool MN>
 int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   using C = Fp8Cfg<BN, MN>;
   const int64_t inner = MN ? a.N : a.K, outer = MN ? a.K : a.N;
-  CUtensorMap tm_x, tm_w;
+  CUtensorMap tm_x, tm_w, tm_y;
   {
     const uint64_t dims[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(a.S)};
     const uint64_t strides[1] = {static_cast<uint64_t>(inner)};
@@ -601,6 +622,15 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     const uint32_t box[3] = {128, MN ? kDepth : BN, 1};
     if (!encode_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) {
       *msg = "tensor map encoding failed for W";
+      return -1;
+    }
+  }
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(outer), static_cast<uint64_t>(a.S)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(outer) * 2};
+    const uint32_t box[2] = {64, 32};
+    if (!encode_map(&tm_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) {
+      *msg = "tensor map encoding failed for the output";
       return -1;
     }
   }
@@ -630,8 +660,8 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     *msg = "too many output tiles";
     return -1;
   }
-  static_assert(C::kRing + kOutBytes + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
-  const size_t smem = static_cast<size_t>(C::kRing) + kOutBytes + sizeof(Fp8Shared) + 1024;
+  static_assert(C::kRing + C::kOutBytes + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
+  const size_t smem = static_cast<size_t>(C::kRing) + C::kOutBytes + sizeof(Fp8Shared) + 1024;
   auto kern = bsq_fp8_kernel<BN, MN>;
   static std::atomic<uint64_t> ready;   // devices (one bit each) on which the kernel is set up
   int dev = 0;
@@ -670,7 +700,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
   cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? tiles * p.split : tiles < a.num_sms ? tiles : a.num_sms));
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, tm_y, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);
