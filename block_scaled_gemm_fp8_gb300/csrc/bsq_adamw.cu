@@ -64,6 +64,7 @@ struct AdamwTable {
   int32_t count;
   float b1, c1m, b2, c2m;   // betas and 1 - betas
   float lr1, rc2, eps;      // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  float one;
   uint32_t salt;            // seed and step
   const float* grad_scale;
 };
@@ -100,6 +101,12 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
       : "r"(h));
   return f;
 }
+
+// Products and sums of two floats an instruction, each rounded by itself.  A packed product
+// and the packed sum it goes to are fused by the assembler, rounding modes notwithstanding;
+// so the sum is a fused multiply-add itself, by a one that only the host knows.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b, float one) { return __ffma2_rn(a, make_float2(one, one), b); }
 
 // 1 / x within 1 ulp; an x below 2^-126 counts as zero.
 __device__ __forceinline__ float reciprocal(float x) {
@@ -222,19 +229,19 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
     auto two = [](float x) { return make_float2(x, x); };
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const float2 gj = __fmul2_rn(make_float2(g[j], g[j + 1]), two(gs));
+      const float2 gj = mul2(make_float2(g[j], g[j + 1]), two(gs));
       float2 mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]);
       if (S8) {
-        mj = __fmul2_rn(mj, two(ms));
-        vj = __fmul2_rn(vj, two(vs));
-        vj = __fmul2_rn(vj, vj);
+        mj = mul2(mj, two(ms));
+        vj = mul2(vj, two(vs));
+        vj = mul2(vj, vj);
       }
-      mj = __fadd2_rn(__fmul2_rn(mj, two(t.b1)), __fmul2_rn(gj, two(t.c1m)));
-      vj = __fadd2_rn(__fmul2_rn(vj, two(t.b2)), __fmul2_rn(__fmul2_rn(gj, gj), two(t.c2m)));
+      mj = add2(mul2(mj, two(t.b1)), mul2(gj, two(t.c1m)), t.one);
+      vj = add2(mul2(vj, two(t.b2)), mul2(mul2(gj, gj), two(t.c2m)), t.one);
       const float2 rj = make_float2(__fsqrt_rn(vj.x), __fsqrt_rn(vj.y));
-      const float2 den = __fadd2_rn(__fmul2_rn(rj, two(t.rc2)), two(t.eps));
-      const float2 u = __fmul2_rn(__fmul2_rn(mj, two(t.lr1)), make_float2(reciprocal(den.x), reciprocal(den.y)));
-      const float2 pj = __fadd2_rn(__fmul2_rn(make_float2(p[j], p[j + 1]), two(e.decay)), make_float2(-u.x, -u.y));
+      const float2 den = add2(mul2(rj, two(t.rc2)), two(t.eps), t.one);
+      const float2 u = mul2(mul2(mj, two(t.lr1)), make_float2(reciprocal(den.x), reciprocal(den.y)));
+      const float2 pj = add2(mul2(make_float2(p[j], p[j + 1]), two(e.decay)), make_float2(-u.x, -u.y), t.one);
       p[j] = pj.x, p[j + 1] = pj.y;
       m[j] = mj.x, m[j + 1] = mj.y;
       v[j] = vj.x, v[j + 1] = vj.y;
@@ -266,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
       for (int j = 0; j < 8; ++j) {
         const uint32_t bits = element_bits(at + j, t.salt);
         if ((j & 1) == 0) {
-          const float2 mj = __fmul2_rn(make_float2(m[j], m[j + 1]), two(im)), rj = __fmul2_rn(make_float2(r[j], r[j + 1]), two(ir));
+          const float2 mj = mul2(make_float2(m[j], m[j + 1]), two(im)), rj = mul2(make_float2(r[j], r[j + 1]), two(ir));
           m[j] = mj.x, m[j + 1] = mj.y;
           r[j] = rj.x, r[j + 1] = rj.y;
         }
@@ -342,6 +349,7 @@ int launch_tables(const AdamwArgs& a, const char** msg) {
   t.lr1 = static_cast<float>(a.lr / (1.0 - std::pow(a.beta1, static_cast<double>(a.step))));
   t.rc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(a.beta2, static_cast<double>(a.step))));
   t.eps = static_cast<float>(a.eps);
+  t.one = 1.f;
   t.salt = a.seed + static_cast<uint32_t>(a.step) * 0x7F4A7C15u;
   t.grad_scale = a.grad_scale;
   int i = 0;

@@ -210,7 +210,6 @@ __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint32_t p0, uint32_t p
 // ones.  One statement, ended by the wait, for the reason tmem_ld_32x32b_x16_wait gives.
 __device__ __forceinline__ void tmem_ld_x32_fma(uint32_t taddr, uint32_t (&next)[32], uint64_t* acc, const uint32_t (&cur)[32],
                                                 uint64_t s2) {
-  __syncwarp();
   asm volatile(
       "{\n\t.reg .b64 p;\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -471,6 +470,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
       // the next accumulator and its scale
       auto arrived = [&]() {
         const bool there = wait8_promote(tfull0 + 8 * bi, bp, abort_flag);
+        __syncwarp();
         tc_fence_after();
         asm volatile("{\n\t.reg .b32 s;\n\tld.shared.b32 s, [%1];\n\tmov.b64 %0, {s, s};\n\t}"
                      : "=l"(s2)

@@ -108,6 +108,54 @@ def test_one_step(bits, grad, offset, wd, step):
             check_codes(t["v"], t["vs"], v.sqrt())
 
 
+def in_float32(t, step, gs, seed):
+    """The states after a step in float32 tensor operations, each rounded by itself: (m, v) or (m
+    codes, m scales, v codes, v scales) of a tensor whose counter starts at 0."""
+    b1, b2 = BETAS
+    g = t["g"].float() * gs
+    f = lambda c, s: c.view(torch.float8_e4m3fn).float() * s.repeat_interleave(B)[:c.numel()]  # noqa: E731
+    m, v = (t["m"], t["v"]) if t["ms"] is None else (f(t["m"], t["ms"]), f(t["v"], t["vs"]).square())
+    m = m * b1 + g * (1 - b1)
+    v = v * b2 + (g * g) * (1 - b2)
+    if t["ms"] is None:
+        return m, v
+    mask, n = 0xFFFFFFFF, m.numel()
+    x = (torch.arange(n, device="cuda") * 0x9E3779B1 + ((seed + step * 0x7F4A7C15) & mask)) & mask
+    x = ((x ^ (x >> 16)) * 0x85EBCA6B) & mask
+    x = ((x ^ (x >> 13)) * 0xC2B2AE35) & mask
+    x = x ^ (x >> 16)
+    got = []
+    for y, bits, keep in ((m, x & 0xFFFF, False), (v.sqrt(), x >> 16, True)):
+        pad = torch.zeros(-(-n // B) * B, device="cuda")
+        pad[:n] = y
+        a = pad.view(-1, B).abs().amax(1)
+        a = torch.where(a == 0, torch.full_like(a, 448.0), a.clamp(min=2.0 ** -100))
+        top = torch.full_like(a, 448.0)
+        q = y * (top / a).repeat_interleave(B)[:n]
+        w = q.abs()
+        big = ((w.view(torch.int32).long() + (bits << 4)) & ~0xFFFFF).to(torch.int32).view(torch.float32)
+        r = torch.where(w >= 2.0 ** -6, big, torch.floor(w * 512 + bits.float() * 2.0 ** -16) * 2.0 ** -9).clamp(max=448.0)
+        if keep:
+            r = torch.where((q > 0) & (r == 0), torch.full_like(r, 2.0 ** -9), r)
+        got += [torch.copysign(r, q), a / top]
+    return got
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_states_follow_float32_bit_for_bit(bits, grad, offset):
+    """No operation of the states is fused with another: they equal the same formula in float32
+    tensor operations (the 8-bit codes by value: a zero has two)."""
+    t = make(300001, grad, bits, 90, offset)
+    want = in_float32(t, 5, 0.75, 11)
+    bsq.adamw(table([t]), 5, LR, BETAS, EPS, grad_scale=torch.full((1,), 0.75, device="cuda"), seed=11)
+    got = (t["m"], t["v"]) if bits == 32 else (t["m"].view(torch.float8_e4m3fn).float(), t["ms"],
+                                               t["v"].view(torch.float8_e4m3fn).float(), t["vs"])
+    for a, b in zip(got, want):
+        assert torch.equal(a + 0.0, b + 0.0), (a != b).sum()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_more_tensors_than_one_launch(bits):
     ts = [make(5 + 37 * i % 300, torch.float32, bits, i) for i in range(600)]
