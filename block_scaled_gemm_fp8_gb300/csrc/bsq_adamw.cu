@@ -1,5 +1,5 @@
 // bsq_adamw.cu -- one AdamW step (decoupled weight decay, Loshchilov and Hutter 2019) over many
-// tensors in one launch per 256 of them, FP32 parameters, states in 32 or in 8 bits:
+// tensors in one launch per 400 of them, FP32 parameters, states in 32 or in 8 bits:
 //
 //   g = grad * grad_scale
 //   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2        r = sqrt(v)
@@ -33,9 +33,9 @@ namespace {
 
 constexpr int kThreadsA = 256;
 constexpr int kStepA = kThreadsA * 8;      // elements of one sweep of a CTA
-// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (146 M elements: 470
+// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (146 M elements: 465
 // us, 5.0 TB/s; 541 of one sweep); with 32-bit ones, where instructions do not count, one
-// (300 small tensors, 5.7 M elements: 29.5 us against 37.3 of two).  Loading a sweep ahead in
+// (300 small tensors, 5.7 M elements: 29.4 us against 37.3 of two).  Loading a sweep ahead in
 // registers changed nothing (472 us).
 template <bool S8>
 constexpr int kSweeps = S8 ? 8 : 1;

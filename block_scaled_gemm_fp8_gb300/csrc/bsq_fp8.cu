@@ -20,14 +20,16 @@
 //   warp 9      MMA issuer
 //   warps 10-11 scales: xs * ws of each k-block's rows and column halves, into shared memory
 // A 128-deep block of BN = 256 takes 512 tensor-core cycles per SM; its promotion is 64 packed
-// FMAs and 4 TMEM loads per thread, 256 cycles of each SM quarter's FMA pipe.  What bounds
-// the kernel is the hand-over of the accumulators: TMEM holds two of them (2 x 256
-// columns), and a k-block takes about 1000 cycles from MMA to promotion and back.  Measured,
-// M = 8192, N = 14336, K = 5120: 500 us, 2.4 PFLOP/s (1.26 of the measured BF16 burst
-// rate); without the promotion's FMAs 454 us, without the MMAs and TMA loads 403 us.
+// FMAs and 4 TMEM loads per thread, 256 cycles of each SM quarter's FMA pipe.  Measured, M =
+// 8192, N = 14336, K = 5120: 440 us, 2.73 PFLOP/s (1.44 of the measured BF16 burst rate).
+// With parts left out, the same product takes 437 us without promotion, 399 without output,
+// 385 without TMA loads, 334 with the MMAs alone and 334 with the promotion alone: the
+// operands' way from L2 to shared memory (48 KB a k-block and SM) bounds it first, what is
+// left is the two accumulators' hand-over (TMEM holds no third of 256 columns).
 // Tried and slower there: CTA pairs of 256 x 256 (585 us: the hand-over crosses SMs), two
-// 128-column accumulators a k-block (504 to 631 us), 16 promotion warps (513 us), one scale
-// load per thread in the promotion loop instead of the scale warps (531 us).
+// 128-column accumulators a k-block with an issuer each (501 us), 16 promotion warps (513 us),
+// one scale load per thread in the promotion loop instead of the scale warps (531 us), scalar
+// FMAs (500 us); a fourth ring stage changed nothing.
 #include <atomic>
 #include <cstdlib>
 
@@ -56,17 +58,14 @@ constexpr int kDepth = 128;                 // contraction per k-block: one scal
 constexpr int kABytes = kRows8 * kDepth;    // 16 KB
 constexpr int kTmemCols8 = 512;
 constexpr int kPromoteWarps = 8, kScaleWarps = 2;
-constexpr int kMaxStages8 = 6;
-constexpr int kMaxBufs8 = 4;
 constexpr int kBoxBytes8 = 32 * 128;        // output box: 32 rows of 64 columns
 constexpr int kMaxSplit = 4;                // clusters of 8 do not all fit the SMs at once
 
-// BN: output columns of a tile.  MN: W is contracted over its rows (dgrad).
-template <int BN, bool MN>
+constexpr int BN = 256;                     // output columns of a tile
 struct Fp8Cfg {
   static constexpr int kBBytes = BN * kDepth;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 3 : 4;
+  static constexpr int kStages = 3;
   static constexpr int kBufs = kTmemCols8 / BN;         // accumulators in TMEM
   static constexpr int kCols = BN / 2;                  // output columns of one promotion warp
   static constexpr int kRing = kStages * kStage;
@@ -90,12 +89,12 @@ struct Fp8Params {
 };
 
 struct Fp8Shared {
-  uint64_t full[kMaxStages8];
-  uint64_t empty[kMaxStages8];
-  uint64_t tmem_full[kMaxBufs8];    // the accumulator is complete and its scales are stored
-  uint64_t tmem_empty[kMaxBufs8];
+  uint64_t full[Fp8Cfg::kStages];
+  uint64_t empty[Fp8Cfg::kStages];
+  uint64_t tmem_full[Fp8Cfg::kBufs];    // the accumulator is complete and its scales are stored
+  uint64_t tmem_empty[Fp8Cfg::kBufs];
   uint64_t drain;
-  float scale[kMaxBufs8][2][kRows8];   // of an accumulator: column half, row
+  float scale[Fp8Cfg::kBufs][2][kRows8];   // of an accumulator: column half, row
   uint32_t tmem_base;
   uint32_t abort_flag;
   int32_t total_mt;                 // row tiles of all experts; none when the offsets are bad
@@ -255,11 +254,12 @@ struct Tile8 {
   int e, row0, row_end, n0;
 };
 
-template <int BN, bool MN>
+// MN: W is contracted over its rows (dgrad).
+template <bool MN>
 __global__ void __launch_bounds__(kThreads8, 1)
     bsq_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, const Fp8Params p) {
-  using C = Fp8Cfg<BN, MN>;
+  using C = Fp8Cfg;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Fp8Shared& sh = *reinterpret_cast<Fp8Shared*>(smem + C::kRing + C::kOutBytes);
@@ -602,9 +602,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
   if (warp == 9) tmem_dealloc(tmem_base, kTmemCols8);
 }
 
-template <int BN, bool MN>
+template <bool MN>
 int launch_fp8_typed(const Fp8Args& a, const char** msg) {
-  using C = Fp8Cfg<BN, MN>;
+  using C = Fp8Cfg;
   const int64_t inner = MN ? a.N : a.K, outer = MN ? a.K : a.N;
   CUtensorMap tm_x, tm_w, tm_y;
   {
@@ -662,7 +662,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   }
   static_assert(C::kRing + C::kOutBytes + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
   const size_t smem = static_cast<size_t>(C::kRing) + C::kOutBytes + sizeof(Fp8Shared) + 1024;
-  auto kern = bsq_fp8_kernel<BN, MN>;
+  auto kern = bsq_fp8_kernel<MN>;
   static std::atomic<uint64_t> ready;   // devices (one bit each) on which the kernel is set up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -712,7 +712,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
 }  // namespace
 
 int launch_fp8(const Fp8Args& a, const char** msg) {
-  return a.dgrad ? launch_fp8_typed<256, true>(a, msg) : launch_fp8_typed<256, false>(a, msg);
+  return a.dgrad ? launch_fp8_typed<true>(a, msg) : launch_fp8_typed<false>(a, msg);
 }
 
 }  // namespace bsq

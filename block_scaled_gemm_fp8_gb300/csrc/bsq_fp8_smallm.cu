@@ -183,13 +183,15 @@ int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
 
 }  // namespace
 
-// Up to 16 rows: one pass over W.  Up to 32: two, the second from L2, while W is small enough
-// to stay there beside what else runs (4096 x 4096, 32 rows: 11.2 us against 13.4 of the
-// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: batches of a few rows
-// each.  32-bit offsets within 32 rows bound K.
+// Dense, up to 16 rows: one pass over W.  Up to 32: two, the second from L2, while W is small
+// enough to stay there beside what else runs (4096 x 4096, 32 rows: 11.2 us against 13.4 of the
+// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: up to one row each on
+// average (64 experts of 2816 x 2048: 32 rows 29.0 us against 37.5, 64 skewed ones 35.0 against
+// 39.4, 64 even ones 45.4 against 42.9, 128 44.0 against 40.9; 16 of 1024 x 4096, 16 rows: 12.3
+// against 20.6).  32-bit offsets within 32 rows bound K.
 bool fp8_takes_smallm(const Fp8Args& a) {
   if (a.dgrad || a.K > (1 << 26)) return false;
-  if (a.offsets) return a.S <= 4 * a.E;
+  if (a.offsets) return a.S <= a.E;
   return a.S <= 16 || (a.S <= 32 && a.N * a.K <= (1 << 25));
 }
 
@@ -209,9 +211,8 @@ int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
   p.kblocks = static_cast<int32_t>((a.K + 127) / 128);
   // With CTAs enough to fill every SM several times over, small CTAs side by side keep more bytes
   // in flight than one that loads ahead, and one's reduction hides behind another's loads
-  // (64 experts of 2816 x 2048, 64 rows: 36 us against 61).
-  // With fewer, one CTA of 16 warps an SM (4096 x 4096: 5.8 us for 8 rows, 7.2 for 16).  An
-  // expert of a decode batch rarely has more than 8 rows.
+  // (14336 x 5120, 8 rows: 15.2 us against 19.5).  With fewer, one CTA of 16 warps an SM (4096
+  // x 4096: 5.8 us for 8 rows, 7.2 for 16).  An expert here rarely has more than 8 rows.
   const bool many = a.offsets || (a.N + kColsS - 1) / kColsS >= 2 * a.num_sms;
   if (a.offsets || a.S <= 8) return many ? launch_typed<1, 8, false, 3>(p, a, msg) : launch_typed<1, 16, true, 1>(p, a, msg);
   return many ? launch_typed<2, 8, false, 2>(p, a, msg) : launch_typed<2, 16, false, 1>(p, a, msg);

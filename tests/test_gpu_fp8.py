@@ -130,6 +130,30 @@ def test_grouped(direction, N, K, counts):
     assert bsq.get_device_error() == (bsq.BSQ_OK, 0)
 
 
+@pytest.mark.parametrize("counts", [[0, 1, 0, 2, 0, 0, 0, 0], [0] * 20 + [1, 0, 19, 0, 0, 9], [1] * 13])
+def test_grouped_few_rows(counts):
+    """No more rows than experts: an expert has none, one, or more than one pass over W takes."""
+    N, K = 264, 400
+    E, S = len(counts), len(counts)
+    used, offs = sum(counts), synth.offsets_from_counts(counts)
+    if used > S:
+        E = S = used
+        offs = np.concatenate([offs, np.full(used - len(counts), used, dtype=offs.dtype)])
+    xc, xs = draw_rows(S, K, 16)
+    xc[used:] = 0x7F
+    wc, ws = draw_weight(E, N, K, 17)
+    y = torch.full((S, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    bsq.fp8_grouped_forward(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), packed(wc, ws),
+                            torch.from_numpy(offs).cuda(), out=y)
+    assert (y[used:] == 7.0).all()
+    x, w = row_values(xc[:used], xs[:used]), weight_values(wc, ws)
+    for e in range(E):
+        r0, r1 = Gm.expert_rows(offs, e)
+        if r1 > r0:
+            check(y[r0:r1], x[r0:r1] @ w[e].T, x[r0:r1], w[e], K, f"expert {e}")
+    assert bsq.get_device_error() == (bsq.BSQ_OK, 0)
+
+
 @pytest.mark.parametrize("M", [4, 20, 300])
 @pytest.mark.parametrize("direction", ["forward", "dgrad"])
 def test_one_hot_is_one_product(direction, M):
@@ -183,6 +207,19 @@ def test_bad_offsets_write_nothing(S):
             st, code = bsq.get_device_error()
             assert (st, code) == (bsq.BSQ_ERR_INVALID_ARG, 2)
             assert (y == 3.0).all()
+
+
+@pytest.mark.parametrize("offs", [[4, 2, 3, 3, 6, 6], [1, 3, 3, 3, 3, 7], [-1, 2, 2, 2, 2, 3]])
+def test_bad_offsets_of_few_rows_write_nothing(offs):
+    """The same with no more rows than experts."""
+    S, N, K = 6, 256, 256
+    xc, xs = draw_rows(S, K, 12)
+    wc, ws = draw_weight(6, N, K, 13)
+    y = torch.full((S, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    bsq.fp8_grouped_forward(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), packed(wc, ws),
+                            torch.tensor(offs, dtype=torch.int32, device="cuda"), out=y)
+    assert bsq.get_device_error() == (bsq.BSQ_ERR_INVALID_ARG, 2)
+    assert (y == 3.0).all()
 
 
 def test_results_repeat_and_streams():
