@@ -5,7 +5,9 @@
 //   scale = a / 448,   code = E4M3(x * (448 / a)), nearest even, saturating at +-448
 //
 // One pass: a block lives in registers between its maximum and its codes, so HBM sees the
-// input once, the codes and the scales.  A NaN in a block makes its scale NaN (maxima are
+// input once, the codes and the scales; HBM bounds it.  Measured: 64 x 2816 x 2048 float32
+// weights 261.5 us, 7.06 TB/s; 8191 x 5120 BF16 activations 21.8 us, 5.8 TB/s (the ramp of a
+// short kernel); 16 x 4096 is all latency, 2 us of the GPU.  A NaN in a block makes its scale NaN (maxima are
 // taken on the bit patterns, where NaN is above infinity); an infinity makes the scale
 // infinite and its own code NaN.
 #include <cuda_bf16.h>
@@ -79,8 +81,8 @@ __device__ __forceinline__ uint2 encode(const Eight<T>& v, float inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// 1 x 128 blocks: 8 lanes of 16 elements per block, four blocks per warp and piece, kChunks
-// pieces loaded before the first is reduced.
+// 1 x 128 blocks: 8 lanes of 16 elements per block (one 16-byte store of codes a lane), four
+// blocks per warp and piece, kChunks pieces loaded before the first is reduced.
 template <typename T>
 __global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_rows_kernel(const T* __restrict__ x, int64_t rows, int cols,
                                                                         int segs, int nblocks, uint8_t* __restrict__ codes,
