@@ -59,6 +59,10 @@ constexpr int kABytes = kRows8 * kDepth;    // 16 KB
 constexpr int kTmemCols8 = 512;
 constexpr int kPromoteWarps = 8, kScaleWarps = 2;
 constexpr int kBoxBytes8 = 32 * 128;        // output box: 32 rows of 64 columns
+// Of the first operand: what stays in L2 beside W and the output (dgrad of 8192 x 14336 x 5120,
+// 117 MB of gradient codes: 465 us in groups, 492 in one; groups of 8 or 16 row tiles where
+// 42 MB fit: 468 and 452 us against 440).
+constexpr int64_t kRasterBytes = 48 << 20;
 constexpr int kMaxSplit = 4;                // clusters of 8 do not all fit the SMs at once
 
 constexpr int BN = 256;                     // output columns of a tile
@@ -83,6 +87,7 @@ struct Fp8Params {
   int32_t* err;
   int32_t S, O, E;
   int32_t kblocks, num_nt;
+  int32_t raster;              // row tiles of a group
   int32_t split;               // CTAs of a cluster that share a tile's contraction; 1: none
   uint64_t timeout_ns;
   int32_t drop_announce;       // test hook: the producer never requests a stage's operands
@@ -333,8 +338,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
   const int tile0 = blockIdx.x / p.split, tile_step = p.split > 1 ? total_tiles : gridDim.x;
   const int kb0 = p.kblocks * rank / p.split, kb1 = p.kblocks * (rank + 1) / p.split;
 
-  // Tile t: experts in order; within one, row tiles vary fastest, so that concurrent CTAs
-  // share W tiles in L2.
+  // Tile t: experts in order; within one, groups of p.raster row tiles; in a group, row tiles
+  // vary fastest, so that concurrent CTAs share W tiles in L2.
   auto tile_of = [&](int t) {
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {
@@ -343,9 +348,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
       else hi = mid - 1;
     }
     const int mts = sh.mt_start[lo + 1] - sh.mt_start[lo];
-    const int l = t - sh.mt_start[lo] * p.num_nt;
+    int l = t - sh.mt_start[lo] * p.num_nt;
+    const int r0 = l / (p.raster * p.num_nt) * p.raster, many = min(p.raster, mts - r0);
+    l -= r0 * p.num_nt;
     const int begin = p.offsets && lo > 0 ? __ldg(p.offsets + lo - 1) : 0;
-    return Tile8{lo, begin + (l % mts) * kRows8, p.offsets ? __ldg(p.offsets + lo) : p.S, (l / mts) * BN};
+    return Tile8{lo, begin + (r0 + l % many) * kRows8, p.offsets ? __ldg(p.offsets + lo) : p.S, (l / many) * BN};
   };
 
   if (warp >= 8) {
@@ -660,6 +667,9 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
     *msg = "too many output tiles";
     return -1;
   }
+  // Every column of tiles reads the group's rows again: from L2, if they stay there.
+  const int64_t groups = a.S * inner / kRasterBytes + 1;
+  p.raster = static_cast<int32_t>((mt + groups - 1) / groups);
   static_assert(C::kRing + C::kOutBytes + sizeof(Fp8Shared) + 1024 <= 232448, "rings exceed the shared memory of a CTA");
   const size_t smem = static_cast<size_t>(C::kRing) + C::kOutBytes + sizeof(Fp8Shared) + 1024;
   auto kern = bsq_fp8_kernel<MN>;

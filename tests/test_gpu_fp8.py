@@ -99,6 +99,26 @@ def test_dgrad(M, N, K):
     assert bsq.get_device_error() == (bsq.BSQ_OK, 0)
 
 
+@pytest.mark.parametrize("direction", ["forward", "dgrad"])
+def test_first_operand_beyond_l2_share(direction):
+    """54 MB of first operand: its row tiles go in groups.  Every output is written, and rows and
+    columns from every tile, the last ones and both sides of the groups' border, are right."""
+    M, inner, outer = 3301, 16384, 528
+    xc, xs = draw_rows(M, inner, 18)
+    wc, ws = draw_weight(1, *((outer, inner) if direction == "forward" else (inner, outer)), 19)
+    y = torch.full((M, outer), float("nan"), dtype=torch.bfloat16, device="cuda")
+    call = bsq.fp8_forward if direction == "forward" else bsq.fp8_dgrad
+    call(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), packed(wc, ws), out=y)
+    assert torch.isfinite(y).all()
+    rows = np.unique(np.concatenate([np.arange(5, M, 97), [0, 1663, 1664, M - 1]]))
+    cols = np.unique(np.concatenate([np.arange(3, outer, 41), [0, 255, 256, outer - 1]]))
+    x, w = row_values(xc[rows], xs[rows]), weight_values(wc, ws)[0]
+    w = w[cols] if direction == "forward" else w[:, cols]
+    check(y[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], x @ (w.T if direction == "forward" else w), x, w,
+          inner, direction)
+    assert bsq.get_device_error() == (bsq.BSQ_OK, 0)
+
+
 ROUTING = [[0, 5, 0, 0, 1], [1, 1, 1, 1], [256, 0, 257, 1, 0, 130], [0, 0, 700], [3] * 40, [64, 0, 8, 15, 2, 33, 128, 300]]
 
 
