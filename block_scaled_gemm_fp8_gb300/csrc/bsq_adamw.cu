@@ -31,12 +31,18 @@ namespace bsq {
 
 namespace {
 
-constexpr int kThreadsA = 256;
-constexpr int kStepA = kThreadsA * 8;      // elements of one sweep of a CTA
-// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (146 M elements: 465
-// us, 5.0 TB/s; 541 of one sweep); with 32-bit ones, where instructions do not count, one
-// (300 small tensors, 5.7 M elements: 29.4 us against 37.3 of two).  Loading a sweep ahead in
-// registers changed nothing (472 us).
+// Small CTAs with 8-bit states: an SM's place is refilled when two warps are done, not eight,
+// which keeps loads in flight beside the rounding's instructions (146 M elements: 396 us, 5.9
+// TB/s; 413 with 128 threads, 441 with 256, 402 with 32).  With 32-bit states large tensors
+// take 583 us with either, 300 small ones 29.4 us with 256 threads and 30.4 with 64, whose
+// CTAs look up their tensor more often.
+template <bool S8>
+constexpr int kThreadsA = S8 ? 64 : 256;
+template <bool S8>
+constexpr int kStepA = kThreadsA<S8> * 8;      // elements of one sweep of a CTA
+// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (396 us; 407 of four
+// sweeps, 397 of 16); with 32-bit ones, where instructions do not count, one (300 small
+// tensors: 29.4 us against 37.3 of two).
 template <bool S8>
 constexpr int kSweeps = S8 ? 8 : 1;
 // Tensors of one launch: the table travels as a kernel parameter, so there are a small one
@@ -153,7 +159,7 @@ __device__ __forceinline__ float lane16_amax(const float (&x)[8]) {
 }
 
 template <bool G16, bool S8, int N>
-__global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_constant__ AdamwTable<N> t) {
+__global__ void __launch_bounds__(kThreadsA<S8>, 1024 / kThreadsA<S8>) adamw_kernel(const __grid_constant__ AdamwTable<N> t) {
   int lo = 0, hi = t.count - 1;
   const int chunk = blockIdx.x;
   while (lo < hi) {
@@ -163,15 +169,17 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
   }
   const AdamwEntry& e = t.e[lo];
   const float gs = t.grad_scale ? __ldg(t.grad_scale) : 1.f;
-  const int64_t first = static_cast<int64_t>(chunk - e.chunk0) * (kSweeps<S8> * kStepA) + threadIdx.x * 8;
+  const int64_t first = static_cast<int64_t>(chunk - e.chunk0) * (kSweeps<S8> * kStepA<S8>) + threadIdx.x * 8;
 #pragma unroll 1
   for (int sweep = 0; sweep < kSweeps<S8>; ++sweep) {
-    const int64_t i0 = first + sweep * kStepA;
+    const int64_t i0 = first + sweep * kStepA<S8>;
     const int64_t left = e.n - i0;
     const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;   // elements of this thread
     const bool wide = e.wide && n == 8;
     if (!S8 && n == 0) return;
+    // as stored; an operand in fewer bits stays packed until its pair is used
     float g[8], p[8], m[8], v[8];
+    uint32_t gw[4] = {}, mw[2] = {}, vw[2] = {};
     float ms = 0.f, vs = 0.f;
     if (S8 && n > 0) {
       ms = e.ms[i0 >> 7];
@@ -181,28 +189,15 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
       ld8(e.p + i0, p);
       if (G16) {
         const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.g) + i0));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          g[2 * j] = __uint_as_float(u[j] << 16);
-          g[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
+        gw[0] = w.x, gw[1] = w.y, gw[2] = w.z, gw[3] = w.w;
       } else {
         ld8(static_cast<const float*>(e.g) + i0, g);
       }
       if (S8) {
         const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(e.m) + i0);
         const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(e.v) + i0);
-        const uint32_t um[4] = {cm.x & 0xFFFFu, cm.x >> 16, cm.y & 0xFFFFu, cm.y >> 16};
-        const uint32_t uv[4] = {cv.x & 0xFFFFu, cv.x >> 16, cv.y & 0xFFFFu, cv.y >> 16};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 fm = from_e4m3x2(um[j]), fv = from_e4m3x2(uv[j]);
-          m[2 * j] = fm.x;
-          m[2 * j + 1] = fm.y;
-          v[2 * j] = fv.x;
-          v[2 * j + 1] = fv.y;
-        }
+        mw[0] = cm.x, mw[1] = cm.y;
+        vw[0] = cv.x, vw[1] = cv.y;
       } else {
         ld8(static_cast<const float*>(e.m) + i0, m);
         ld8(static_cast<const float*>(e.v) + i0, v);
@@ -213,10 +208,11 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
         p[j] = g[j] = m[j] = v[j] = 0.f;
         if (j < n) {
           p[j] = e.p[i0 + j];
-          g[j] = G16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[i0 + j]) : static_cast<const float*>(e.g)[i0 + j];
+          if (G16) gw[j / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(e.g)[i0 + j]) << (16 * (j & 1));
+          else g[j] = static_cast<const float*>(e.g)[i0 + j];
           if (S8) {
-            m[j] = from_e4m3x2(static_cast<const uint8_t*>(e.m)[i0 + j]).x;
-            v[j] = from_e4m3x2(static_cast<const uint8_t*>(e.v)[i0 + j]).x;
+            mw[j / 4] |= static_cast<uint32_t>(static_cast<const uint8_t*>(e.m)[i0 + j]) << (8 * (j & 3));
+            vw[j / 4] |= static_cast<uint32_t>(static_cast<const uint8_t*>(e.v)[i0 + j]) << (8 * (j & 3));
           } else {
             m[j] = static_cast<const float*>(e.m)[i0 + j];
             v[j] = static_cast<const float*>(e.v)[i0 + j];
@@ -229,11 +225,12 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
     auto two = [](float x) { return make_float2(x, x); };
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const float2 gj = mul2(make_float2(g[j], g[j + 1]), two(gs));
-      float2 mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]);
+      float2 gj = make_float2(g[j], g[j + 1]), mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]);
+      if (G16) gj = make_float2(__uint_as_float(gw[j / 2] << 16), __uint_as_float(gw[j / 2] & 0xFFFF0000u));
+      gj = mul2(gj, two(gs));
       if (S8) {
-        mj = mul2(mj, two(ms));
-        vj = mul2(vj, two(vs));
+        mj = mul2(from_e4m3x2(mw[j / 4] >> (8 * (j & 3)) & 0xFFFFu), two(ms));
+        vj = mul2(from_e4m3x2(vw[j / 4] >> (8 * (j & 3)) & 0xFFFFu), two(vs));
         vj = mul2(vj, vj);
       }
       mj = add2(mul2(mj, two(t.b1)), mul2(gj, two(t.c1m)), t.one);
@@ -246,6 +243,26 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
       m[j] = mj.x, m[j + 1] = mj.y;
       v[j] = vj.x, v[j + 1] = vj.y;
       r[j] = rj.x, r[j + 1] = rj.y;
+    }
+    // the parameters are stored before the states are rounded, which wants their registers
+    if (wide) {
+      st8(e.p + i0, p);
+      if (e.copy) {
+        uint4 w;
+        w.x = bf16x2(p[0], p[1]);
+        w.y = bf16x2(p[2], p[3]);
+        w.z = bf16x2(p[4], p[5]);
+        w.w = bf16x2(p[6], p[7]);
+        *reinterpret_cast<uint4*>(e.copy + i0) = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < n) {
+          e.p[i0 + j] = p[j];
+          if (e.copy) e.copy[i0 + j] = __float2bfloat16_rn(p[j]);
+        }
+      }
     }
     if (S8 && n < 8) {
 #pragma unroll
@@ -267,48 +284,37 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
       const int64_t block = (i0 - (upper ? 64 : 0)) >> 7;
       if ((lane & 7) == 0 && (block << 7) < e.n) (upper ? e.vs : e.ms)[block] = scale;
       const uint32_t at = e.counter + static_cast<uint32_t>(i0);
-      float qm[8], qr[8];
       float least = 1.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t bits = element_bits(at + j, t.salt);
-        if ((j & 1) == 0) {
-          const float2 mj = mul2(make_float2(m[j], m[j + 1]), two(im)), rj = mul2(make_float2(r[j], r[j + 1]), two(ir));
-          m[j] = mj.x, m[j + 1] = mj.y;
-          r[j] = rj.x, r[j + 1] = rj.y;
-        }
-        const float am_j = fabsf(m[j]);
-        least = fminf(least, fminf(am_j, r[j]));
-        qm[j] = copysignf(round_normal(am_j, bits & 0xFFFFu), m[j]);
-        qr[j] = round_normal(r[j], bits >> 16);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 mj = mul2(make_float2(m[j], m[j + 1]), two(im)), rj = mul2(make_float2(r[j], r[j + 1]), two(ir));
+        const uint32_t b0 = element_bits(at + j, t.salt), b1 = element_bits(at + j + 1, t.salt);
+        m[j] = mj.x, m[j + 1] = mj.y;
+        r[j] = rj.x, r[j + 1] = rj.y;
+        least = fminf(least, fminf(fminf(fabsf(mj.x), rj.x), fminf(fabsf(mj.y), rj.y)));
+        cm[j / 2] = e4m3x2(copysignf(round_normal(fabsf(mj.x), b0 & 0xFFFFu), mj.x),
+                           copysignf(round_normal(fabsf(mj.y), b1 & 0xFFFFu), mj.y));
+        cv[j / 2] = e4m3x2(round_normal(rj.x, b0 >> 16), round_normal(rj.y, b1 >> 16));
       }
       // Below 2^-6 (2^-15 of the block's largest: rare), or NaN, which only a NaN or infinite
       // scale leaves: once more in full.
       if (!(least >= 0.015625f) || !(inv > 0.f)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t bits = element_bits(at + j, t.salt);
-          qm[j] = copysignf(round_any(fabsf(m[j]), bits & 0xFFFFu), m[j]);
-          const float q = round_any(r[j], bits >> 16);
-          qr[j] = r[j] > 0.f && q == 0.f ? 1.953125e-3f : q;
-        }
-      }
+        for (int j = 0; j < 8; j += 2) {
+          float qm[2], qr[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cm[j] = e4m3x2(qm[2 * j], qm[2 * j + 1]);
-        cv[j] = e4m3x2(qr[2 * j], qr[2 * j + 1]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t bits = element_bits(at + j + h, t.salt);
+            qm[h] = copysignf(round_any(fabsf(m[j + h]), bits & 0xFFFFu), m[j + h]);
+            const float q = round_any(r[j + h], bits >> 16);
+            qr[h] = r[j + h] > 0.f && q == 0.f ? 1.953125e-3f : q;
+          }
+          cm[j / 2] = e4m3x2(qm[0], qm[1]);
+          cv[j / 2] = e4m3x2(qr[0], qr[1]);
+        }
       }
     }
     if (wide) {
-      st8(e.p + i0, p);
-      if (e.copy) {
-        uint4 w;
-        w.x = bf16x2(p[0], p[1]);
-        w.y = bf16x2(p[2], p[3]);
-        w.z = bf16x2(p[4], p[5]);
-        w.w = bf16x2(p[6], p[7]);
-        *reinterpret_cast<uint4*>(e.copy + i0) = w;
-      }
       if (S8) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + i0) = make_uint2(cm[0] | (cm[1] << 16), cm[2] | (cm[3] << 16));
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + i0) = make_uint2(cv[0] | (cv[1] << 16), cv[2] | (cv[3] << 16));
@@ -320,8 +326,6 @@ __global__ void __launch_bounds__(kThreadsA, 4) adamw_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j < n) {
-          e.p[i0 + j] = p[j];
-          if (e.copy) e.copy[i0 + j] = __float2bfloat16_rn(p[j]);
           if (S8) {
             static_cast<uint8_t*>(e.m)[i0 + j] = static_cast<uint8_t>(cm[j >> 1] >> (8 * (j & 1)));
             static_cast<uint8_t*>(e.v)[i0 + j] = static_cast<uint8_t>(cv[j >> 1] >> (8 * (j & 1)));
@@ -359,7 +363,7 @@ int launch_tables(const AdamwArgs& a, const char** msg) {
     for (; i < a.count && t.count < N; ++i) {
       const bsq_adamw_tensor& s = ts[i];
       if (s.n == 0) continue;
-      const int64_t chunk = static_cast<int64_t>(s8 ? kSweeps<true> : kSweeps<false>) * kStepA;
+      const int64_t chunk = s8 ? kSweeps<true> * kStepA<true> : kSweeps<false> * kStepA<false>;
       const int64_t c = (s.n + chunk - 1) / chunk;
       if (chunks + c > INT32_MAX) break;   // the next launch takes it
       AdamwEntry& e = t.e[t.count++];
@@ -379,10 +383,10 @@ int launch_tables(const AdamwArgs& a, const char** msg) {
     }
     if (t.count == 0) break;
     const dim3 grid(static_cast<unsigned>(chunks));
-    if (g16 && s8) adamw_kernel<true, true, N><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else if (g16) adamw_kernel<true, false, N><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else if (s8) adamw_kernel<false, true, N><<<grid, kThreadsA, 0, a.stream>>>(t);
-    else adamw_kernel<false, false, N><<<grid, kThreadsA, 0, a.stream>>>(t);
+    if (g16 && s8) adamw_kernel<true, true, N><<<grid, kThreadsA<true>, 0, a.stream>>>(t);
+    else if (g16) adamw_kernel<true, false, N><<<grid, kThreadsA<false>, 0, a.stream>>>(t);
+    else if (s8) adamw_kernel<false, true, N><<<grid, kThreadsA<true>, 0, a.stream>>>(t);
+    else adamw_kernel<false, false, N><<<grid, kThreadsA<false>, 0, a.stream>>>(t);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
       *msg = cudaGetErrorString(e);
