@@ -212,9 +212,18 @@ int launch_fp8_smallm(const Fp8Args& a, const char** msg) {
   // With CTAs enough to fill every SM several times over, small CTAs side by side keep more bytes
   // in flight than one that loads ahead, and one's reduction hides behind another's loads
   // (14336 x 5120, 8 rows: 15.2 us against 19.5).  With fewer, one CTA of 16 warps an SM (4096
-  // x 4096: 5.8 us for 8 rows, 7.2 for 16).  An expert here rarely has more than 8 rows.
-  const bool many = a.offsets || (a.N + kColsS - 1) / kColsS >= 2 * a.num_sms;
-  if (a.offsets || a.S <= 8) return many ? launch_typed<1, 8, false, 3>(p, a, msg) : launch_typed<1, 16, true, 1>(p, a, msg);
+  // x 4096: 5.8 us for 8 rows, 7.2 for 16).  An expert here rarely has more than 8 rows.  Warps
+  // that would have two or three blocks of a short contraction each spend more on the
+  // reduction than on loads: half as many, six CTAs an SM, if there are CTAs for it (64 experts
+  // of 2816 x 2048: 64 skewed rows 30.7 us against 35.0, 64 even ones 40.6 against 45.5; of
+  // 7168 x 1024: 50.8 against 65.7; but of 2048 x 4096: 60.8 against 57.8; 448 CTAs of a dense
+  // 14336 x 5120: 18.2 against 14.7).
+  const int64_t ctas = (a.N + kColsS - 1) / kColsS * (a.offsets ? a.E : 1);
+  const bool many = a.offsets || ctas >= 2 * a.num_sms;
+  if (a.offsets || a.S <= 8) {
+    if (p.kblocks <= 24 && ctas >= 5 * a.num_sms) return launch_typed<1, 4, false, 6>(p, a, msg);
+    return many ? launch_typed<1, 8, false, 3>(p, a, msg) : launch_typed<1, 16, true, 1>(p, a, msg);
+  }
   return many ? launch_typed<2, 8, false, 2>(p, a, msg) : launch_typed<2, 16, false, 1>(p, a, msg);
 }
 

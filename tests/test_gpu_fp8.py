@@ -229,6 +229,27 @@ def test_bad_offsets_write_nothing(S):
             assert (y == 3.0).all()
 
 
+@pytest.mark.parametrize("K", [16, 400, 2064])
+def test_grouped_many_experts_of_few_rows(K):
+    """CTAs enough for the small ones of a short contraction: most experts empty, one with 11 rows."""
+    E, N = 200, 136
+    counts = np.zeros(E, dtype=np.int64)
+    counts[[3, 50, 51, 120]], counts[77], counts[199] = 1, 11, 4
+    used = int(counts.sum())
+    offs = synth.offsets_from_counts(list(counts))
+    xc, xs = draw_rows(used, K, 20)
+    wc, ws = draw_weight(E, N, K, 21)
+    y = torch.full((used, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    bsq.fp8_grouped_forward(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), packed(wc, ws),
+                            torch.from_numpy(offs).cuda(), out=y)
+    x = row_values(xc, xs)
+    for e in np.flatnonzero(counts):
+        r0, r1 = Gm.expert_rows(offs, int(e))
+        w = weight_values(wc[e:e + 1], ws[e:e + 1])[0]
+        check(y[r0:r1], x[r0:r1] @ w.T, x[r0:r1], w, K, f"expert {e}")
+    assert bsq.get_device_error() == (bsq.BSQ_OK, 0)
+
+
 @pytest.mark.parametrize("offs", [[4, 2, 3, 3, 6, 6], [1, 3, 3, 3, 3, 7], [-1, 2, 2, 2, 2, 3]])
 def test_bad_offsets_of_few_rows_write_nothing(offs):
     """The same with no more rows than experts."""
