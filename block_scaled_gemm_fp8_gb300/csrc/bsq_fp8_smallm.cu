@@ -185,13 +185,13 @@ int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
 
 // Dense, up to 16 rows: one pass over W.  Up to 32: two, the second from L2, while W is small
 // enough to stay there beside what else runs (4096 x 4096, 32 rows: 11.2 us against 13.4 of the
-// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: up to one row each on
-// average (64 experts of 2816 x 2048: 32 rows 29.0 us against 37.5, 64 skewed ones 35.0 against
-// 39.4, 64 even ones 45.4 against 42.9, 128 44.0 against 40.9; 16 of 1024 x 4096, 16 rows: 12.3
-// against 20.6).  32-bit offsets within 32 rows bound K.
+// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: up to two rows each on
+// average (64 experts of 2816 x 2048: 32 rows 26.0 us against 37.5, 64 skewed ones 30.7 against
+// 39.4, 128 42.7 against 40.9, 128 even ones 49.0 against 51.6, 256 59.0 against 54.4; 16 of
+// 4096 x 4096, 32 rows: 36.6 against 47.1).  32-bit offsets within 32 rows bound K.
 bool fp8_takes_smallm(const Fp8Args& a) {
   if (a.dgrad || a.K > (1 << 26)) return false;
-  if (a.offsets) return a.S <= a.E;
+  if (a.offsets) return a.S <= 2 * a.E;
   return a.S <= 16 || (a.S <= 32 && a.N * a.K <= (1 << 25));
 }
 
