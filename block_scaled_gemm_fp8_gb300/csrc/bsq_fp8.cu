@@ -21,15 +21,19 @@
 //   warps 10-11 scales: xs * ws of each k-block's rows and column halves, into shared memory
 // A 128-deep block of BN = 256 takes 512 tensor-core cycles per SM; its promotion is 64 packed
 // FMAs and 4 TMEM loads per thread, 256 cycles of each SM quarter's FMA pipe.  Measured, M =
-// 8192, N = 14336, K = 5120: 440 us, 2.73 PFLOP/s (1.44 of the measured BF16 burst rate).
-// With parts left out, the same product takes 437 us without promotion, 399 without output,
-// 385 without TMA loads, 334 with the MMAs alone and 334 with the promotion alone: the
-// operands' way from L2 to shared memory (48 KB a k-block and SM) bounds it first, what is
-// left is the two accumulators' hand-over (TMEM holds no third of 256 columns).
-// Tried and slower there: CTA pairs of 256 x 256 (585 us: the hand-over crosses SMs), two
-// 128-column accumulators a k-block with an issuer each (501 us), 16 promotion warps (513 us),
-// one scale load per thread in the promotion loop instead of the scale warps (531 us), scalar
-// FMAs (500 us); a fourth ring stage changed nothing.
+// 8192, N = 14336, K = 5120: 438 us, 2.75 PFLOP/s (1.44 of the measured BF16 burst rate).
+// With parts left out, the same product takes 399 us without output, 385 without the
+// promotion's loads and FMAs, 385 without TMA loads, 334 with the MMAs alone and 334 with the
+// promotion alone.  The operands take 48 KB of writes
+// and as many reads of an SM's shared memory a k-block, beside which neither MMAs nor
+// promotion reach their own rate; loading W's tile once for two CTAs (multicast) changed
+// nothing (437 us), so L2 does not bound it.
+// Tried and slower there: CTA pairs of 256 x 256, which halve W's part (509 us, 354 without
+// promotion: an accumulator's hand-over then crosses SMs; 658 in half accumulators); two
+// 128-column accumulators a k-block with an issuer each (501); 16 promotion warps (513); one
+// scale load per thread in the promotion loop instead of the scale warps (531); scalar FMAs
+// (500); L2 prefetch of operands 6 or 16 k-blocks ahead (456, 458); consecutive tiles to one
+// CTA (545).  A fourth ring stage changed nothing.
 #include <atomic>
 #include <cstdlib>
 

