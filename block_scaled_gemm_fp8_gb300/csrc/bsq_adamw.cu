@@ -32,16 +32,16 @@ namespace bsq {
 namespace {
 
 // Small CTAs with 8-bit states: an SM's place is refilled when two warps are done, not eight,
-// which keeps loads in flight beside the rounding's instructions (146 M elements: 396 us, 5.9
-// TB/s; 413 with 128 threads, 441 with 256, 402 with 32).  With 32-bit states large tensors
-// take 583 us with either, 300 small ones 29.4 us with 256 threads and 30.4 with 64, whose
-// CTAs look up their tensor more often.
+// which keeps loads in flight beside the rounding's instructions (146 M elements: 396 us; 413
+// with 128 threads, 441 with 256, 402 with 32; with the instructions saved since, 382 us, 6.1
+// TB/s).  With 32-bit states large tensors take 583 us with either, 300 small ones 29.4 us with
+// 256 threads and 30.4 with 64, whose CTAs look up their tensor more often.
 template <bool S8>
 constexpr int kThreadsA = S8 ? 64 : 256;
 template <bool S8>
 constexpr int kStepA = kThreadsA<S8> * 8;      // elements of one sweep of a CTA
-// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (396 us; 407 of four
-// sweeps, 397 of 16); with 32-bit ones, where instructions do not count, one (300 small
+// Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (384 us on the
+// device; 389 of six sweeps, 383 of twelve); with 32-bit ones, where instructions do not count, one (300 small
 // tensors: 29.4 us against 37.3 of two).
 template <bool S8>
 constexpr int kSweeps = S8 ? 8 : 1;
@@ -129,10 +129,11 @@ __device__ __forceinline__ uint32_t element_bits(uint32_t i, uint32_t salt) {
   return x ^ (x >> 16);
 }
 
-// E4M3 magnitude next to a, up with the probability of the part cut off: 16 random bits
-// against the mantissa bits below E4M3's three.  For 2^-6 <= a <= 448 and a little above.
+// E4M3 value next to a, away from zero with the probability of the part cut off: 16 random bits
+// against the mantissa bits below E4M3's three.  For magnitudes from 2^-6 to 448 and a little
+// above; what comes out above 448 the conversion takes back to it.
 __device__ __forceinline__ float round_normal(float a, uint32_t bits) {
-  return fminf(__uint_as_float((__float_as_uint(a) + (bits << 4)) & 0xFFF00000u), 448.f);
+  return __uint_as_float((__float_as_uint(a) + (bits << 4)) & 0xFFF00000u);
 }
 // The same for every a >= 0 (NaN stays): below 2^-6, against the part below the subnormal
 // step of 2^-9.  x + 2^23 rounded down, less 2^23, is the floor of an x below 2^22.
@@ -147,12 +148,25 @@ __device__ __forceinline__ float block_amax(float a) {
   return a == 0.f ? 448.f : a < 7.888609052210118e-31f ? 7.888609052210118e-31f : a;   // 2^-100; NaN stays
 }
 
-// Scale block of 16 lanes x 8 values: the block's a from each lane's largest magnitude
-// (bit patterns: NaN is above infinity).
+// Largest and smallest of three; the largest is NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Scale block of 16 lanes x 8 values: the block's a from each lane's largest magnitude (bit
+// patterns between lanes: NaN is above infinity).
 __device__ __forceinline__ float lane16_amax(const float (&x)[8]) {
-  uint32_t m = 0;
+  float f = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 8; i += 2) f = max3_nan(f, fabsf(x[i]), fabsf(x[i + 1]));
+  uint32_t m = __float_as_uint(f);
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   return block_amax(__uint_as_float(m));
@@ -291,9 +305,8 @@ __global__ void __launch_bounds__(kThreadsA<S8>, 1024 / kThreadsA<S8>) adamw_ker
         const uint32_t b0 = element_bits(at + j, t.salt), b1 = element_bits(at + j + 1, t.salt);
         m[j] = mj.x, m[j + 1] = mj.y;
         r[j] = rj.x, r[j + 1] = rj.y;
-        least = fminf(least, fminf(fminf(fabsf(mj.x), rj.x), fminf(fabsf(mj.y), rj.y)));
-        cm[j / 2] = e4m3x2(copysignf(round_normal(fabsf(mj.x), b0 & 0xFFFFu), mj.x),
-                           copysignf(round_normal(fabsf(mj.y), b1 & 0xFFFFu), mj.y));
+        least = min3(min3(least, fabsf(mj.x), rj.x), fabsf(mj.y), rj.y);
+        cm[j / 2] = e4m3x2(round_normal(mj.x, b0 & 0xFFFFu), round_normal(mj.y, b1 & 0xFFFFu));
         cv[j / 2] = e4m3x2(round_normal(rj.x, b0 >> 16), round_normal(rj.y, b1 >> 16));
       }
       // Below 2^-6 (2^-15 of the block's largest: rare), or NaN, which only a NaN or infinite
