@@ -41,8 +41,8 @@ constexpr int kThreadsA = S8 ? 64 : 256;
 template <bool S8>
 constexpr int kStepA = kThreadsA<S8> * 8;      // elements of one sweep of a CTA
 // Sweeps of a CTA: with 8-bit states, enough to pay for finding its tensor (384 us on the
-// device; 389 of six sweeps, 383 of twelve); with 32-bit ones, where instructions do not count, one (300 small
-// tensors: 29.4 us against 37.3 of two).
+// device; 388 of six sweeps, 383 of twelve); with 32-bit ones, where instructions do not count,
+// one (300 small tensors: 29.4 us against 37.3 of two).
 template <bool S8>
 constexpr int kSweeps = S8 ? 8 : 1;
 // Tensors of one launch: the table travels as a kernel parameter, so there are a small one

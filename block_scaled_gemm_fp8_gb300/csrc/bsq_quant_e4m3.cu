@@ -7,7 +7,7 @@
 // One pass: a block lives in registers between its maximum and its codes, so HBM sees the
 // input once, the codes and the scales; HBM bounds it.  Measured: 64 x 2816 x 2048 float32
 // weights 261.5 us, 7.06 TB/s; 8191 x 5120 BF16 activations 21.8 us, 5.8 TB/s (the ramp of a
-// short kernel); 16 x 4096 is all latency, 2 us of the GPU.  A NaN in a block makes its scale NaN (maxima are
+// short kernel); 16 x 4096 is all latency, 4 us a launch back to back.  A NaN in a block makes its scale NaN (maxima are
 // taken on the bit patterns, where NaN is above infinity); an infinity makes the scale
 // infinite and its own code NaN.
 #include <cuda_bf16.h>
