@@ -188,13 +188,16 @@ int launch_typed(const Fp8SmallParams& p, const Fp8Args& a, const char** msg) {
 
 // Dense, up to 16 rows: one pass over W.  Up to 32: two, the second from L2, while W is small
 // enough to stay there beside what else runs (4096 x 4096, 32 rows: 11.2 us against 13.4 of the
-// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: up to two rows each on
-// average (64 experts of 2816 x 2048: 32 rows 26.0 us against 37.5, 64 skewed ones 30.7 against
-// 39.4, 128 42.7 against 40.9, 128 even ones 49.0 against 51.6, 256 59.0 against 54.4; 16 of
-// 4096 x 4096, 32 rows: 36.6 against 47.1).  32-bit offsets within 32 rows bound K.
+// tensor-core kernel; 14336 x 5120: 36.8 against 24.9).  Per expert: up to 64 rows and
+// one an expert on average (64 experts of 2816 x 2048: 64 skewed rows 30.7 us against 39.4, 64
+// even ones 40.6 against 42.9; of 2048 x 2048: 28.9 against 28.8 and 47.2 against 51.2; but 128
+// skewed rows 45.7 against 32.8, and 256 on 256 experts 73 against 65), up to 32 rows two (16
+// experts of 4096 x 4096, 32 rows: 36.6 against 47.1).  An expert's rows past the eighth cost a
+// pass over its W each eight: were all 64 rows one expert's, 38.5 us against 14.0, which
+// routing to more than one expert a token does not do.  32-bit offsets within 32 rows bound K.
 bool fp8_takes_smallm(const Fp8Args& a) {
   if (a.dgrad || a.K > (1 << 26)) return false;
-  if (a.offsets) return a.S <= 2 * a.E;
+  if (a.offsets) return a.S <= 32 ? a.S <= 2 * a.E : a.S <= 64 && a.S <= a.E;
   return a.S <= 16 || (a.S <= 32 && a.N * a.K <= (1 << 25));
 }
 
