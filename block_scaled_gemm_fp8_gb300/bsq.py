@@ -285,19 +285,28 @@ _DTYPES = {torch.bfloat16: BSQ_DT_BF16, torch.float32: BSQ_DT_F32}
 def quantize_e4m3(x, block_rows=1, codes=None, scale=None, stream=None):
     """(codes u8, scale f32) of x (BF16 or float32, [rows, cols] or [batch, rows, cols]) in blocks of
     block_rows x 128, block_rows 1 (activations, gradients) or 128 (weights)."""
-    _dense(x, _DTYPES, "quantize_e4m3: x")
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or not (x.is_cuda and x.is_contiguous()):
+        _dense(x, _DTYPES, "quantize_e4m3: x")   # says what is wrong
     shape = x.shape
-    if len(shape) == 2:
-        batch, (rows, cols) = 1, shape
-    elif len(shape) == 3:
+    if len(shape) == 3:
         batch, rows, cols = shape
+        blocks = (batch, rows if block_rows == 1 else (rows + 127) // 128, (cols + 127) // 128)
+    elif len(shape) == 2:
+        batch, (rows, cols) = 1, shape
+        blocks = (rows if block_rows == 1 else (rows + 127) // 128, (cols + 127) // 128)
     else:
         raise ValueError(f"quantize_e4m3: x has {len(shape)} dimensions, 2 or 3 are wanted")
-    blocks = (rows if block_rows == 1 else (rows + 127) // 128, (cols + 127) // 128)
-    codes = _out(codes, shape, torch.uint8, x, stream, "quantize_e4m3: codes")
-    scale = _out(scale, blocks if len(shape) == 2 else (batch, *blocks), torch.float32, x, stream, "quantize_e4m3: scale")
-    _check(lib().bsq_quantize_e4m3(_DTYPES[x.dtype], x.data_ptr(), batch, rows, cols, block_rows, codes.data_ptr(),
-                                   scale.data_ptr(), _raw_stream(stream, x)))
+    if stream is None and codes is None and scale is None:
+        codes = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(blocks, dtype=torch.float32, device=x.device)
+    else:
+        codes = _out(codes, shape, torch.uint8, x, stream, "quantize_e4m3: codes")
+        scale = _out(scale, blocks, torch.float32, x, stream, "quantize_e4m3: scale")
+    status = (_lib or lib()).bsq_quantize_e4m3(dtype, x.data_ptr(), batch, rows, cols, block_rows, codes.data_ptr(),
+                                               scale.data_ptr(), _raw_stream(stream, x))
+    if status:
+        _check(status)
     return codes, scale
 
 
@@ -315,19 +324,24 @@ def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
         raise ValueError(f"{name}: codes {tuple(codes.shape)} on {codes.device}, scale {tuple(scale.shape)} on {scale.device}; "
                          f"[rows, {inner}] and [rows, {blocks}] are wanted; w holds {wd.numel()} codes and {ws.numel()} scales "
                          f"on {wd.device} and {ws.device} for [{batch}, {n}, {k}]")
-    out = _out(out, (rows, outer), torch.bfloat16, codes, stream, name)
+    if stream is None and out is None:
+        out = torch.empty((rows, outer), dtype=torch.bfloat16, device=codes.device)
+    else:
+        out = _out(out, (rows, outer), torch.bfloat16, codes, stream, name)
     fn = getattr(_lib or lib(), "bsq_" + name)
     raw = _raw_stream(stream, codes)
     if offsets is None:
         if batch != 1:
             raise ValueError(f"{name}: one weight is wanted, not {batch}")
-        _check(fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), n, k, out.data_ptr(), raw))
+        status = fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), n, k, out.data_ptr(), raw)
     else:
         _dense(offsets, (torch.int32,), name)
         if offsets.numel() != batch or offsets.get_device() != dev:
             raise ValueError(f"{name}: {offsets.numel()} offsets on {offsets.device} for {batch} experts")
-        _check(fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), batch, n, k,
-                  offsets.data_ptr(), out.data_ptr(), raw))
+        status = fn(codes.data_ptr(), scale.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), batch, n, k,
+                    offsets.data_ptr(), out.data_ptr(), raw)
+    if status:
+        _check(status)
     return out
 
 
