@@ -116,6 +116,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bo
          | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Whole-warp roles leave their loops together: a lane that left alone would leave the others at
+// an instruction that wants all 32.  No lane branches on how a wait ended.  Promotion and scale
+// lanes remember a failure, wait no more and go on with the others, and the warp votes once a
+// tile; the MMA warp votes behind each k-block's MMAs, between its two announcements (8192 x
+// 14336 x 5120: 487 us, as without agreement; a vote before the first announcement 489, behind
+// the second 492, right after every wait 500).
+__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // One lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
@@ -402,16 +410,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
       const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
       uint32_t st = 0, sp = 0, bi = 0, bp = 1;   // stage and its parity, TMEM buffer and its empty parity
       bool ok = true;
-      for (int t = tile0; ok && t < total_tiles && !*abort_flag; t += tile_step) {
+      for (int t = tile0; t < total_tiles && all_lanes(ok && !*abort_flag); t += tile_step) {
 #pragma unroll 1
         for (int kb = kb0; kb < kb1; ++kb) {
           ok = wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit) && wait8(full0 + 8 * st, sp, abort_flag, p.err, limit);
-          if (!ok) break;
           __syncwarp();
           tc_fence_after();
           umma_e4m3_k128<MN ? 256 : 2>(elected, tmem_base + bi * BN, adesc0 + st * (C::kStage >> 4),
                                        bdesc0 + st * (C::kStage >> 4), idesc);
           umma_commit(elected, tfull0 + 8 * bi);
+          if (!all_lanes(ok)) break;   // after a failure no operands are asked for
           umma_commit(elected, empty0 + 8 * st);
           if (++bi == C::kBufs) {
             bi = 0;
@@ -429,7 +437,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
       const uint32_t tempty0 = smem_u32(&sh.tmem_empty[0]), tfull0 = smem_u32(&sh.tmem_full[0]);
       uint32_t bi = 0, bp = 1;
       bool ok = true;
-      for (int t = tile0; ok && t < total_tiles && !*abort_flag; t += tile_step) {
+      for (int t = tile0; t < total_tiles && all_lanes(ok && !*abort_flag); t += tile_step) {
         const Tile8 tl = tile_of(t);
         // rows past the expert's last and columns past the last block: not stored, any scale does
         const float* xs0 = p.xs + static_cast<int64_t>(min(tl.row0 + i, tl.row_end - 1)) * p.xs_ld;
@@ -444,14 +452,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
           const float w0 = __ldg(ws0), w1 = __ldg(ws1);
           ws0 += p.ws_c;
           ws1 += p.ws_c;
-          ok = wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit);
-          if (!ok) break;
+          ok = ok && wait8(tempty0 + 8 * bi, bp, abort_flag, p.err, limit);
           sh.scale[bi][0][i] = x0 * w0;
           sh.scale[bi][0][i + 64] = x1 * w0;
           sh.scale[bi][1][i] = x0 * w1;
           sh.scale[bi][1][i + 64] = x1 * w1;
           __syncwarp();
-          if (elected) mbar_arrive(tfull0 + 8 * bi);
+          if (elected && ok) mbar_arrive(tfull0 + 8 * bi);
           if (++bi == C::kBufs) {
             bi = 0;
             bp ^= 1u;
@@ -470,7 +477,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint32_t stage = smem_u32(smem + C::kRing) + warp * C::kOutWarp;
     const uint32_t tfull0 = smem_u32(&sh.tmem_full[0]), tempty0 = smem_u32(&sh.tmem_empty[0]);
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * C::kCols;
-    for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
+    bool ok = true;
+    for (int t = tile0; t < total_tiles && all_lanes(!*abort_flag); t += tile_step) {
       const Tile8 tl = tile_of(t);
       const int col0 = tl.n0 + h * C::kCols;
       uint64_t acc[C::kCols / 2];
@@ -480,16 +488,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
       uint64_t s2;   // the k-block's scale, twice
       // the next accumulator and its scale
       auto arrived = [&]() {
-        const bool there = wait8_promote(tfull0 + 8 * bi, bp, abort_flag);
+        ok = ok && wait8_promote(tfull0 + 8 * bi, bp, abort_flag);
         __syncwarp();
         tc_fence_after();
         asm volatile("{\n\t.reg .b32 s;\n\tld.shared.b32 s, [%1];\n\tmov.b64 %0, {s, s};\n\t}"
                      : "=l"(s2)
                      : "r"(scale0 + bi * (2 * kRows8 * 4))
                      : "memory");
-        return there;
       };
-      if (!arrived()) goto promoted;   // aborted: nothing is stored
+      arrived();
       tmem_ld_32x32b_x32_wait(trow + bi * BN, v[0]);
 #pragma unroll 1
       for (int left = kb1 - kb0; left > 0; --left) {
@@ -506,13 +513,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
           bp ^= 1u;
         }
         if (left > 1) {
-          if (!arrived()) goto promoted;
+          arrived();
           tmem_ld_x32_fma(trow + bi * BN, v[0], acc + (kChunks - 1) * 16, v[1], s);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) fma_f32x2(acc[(kChunks - 1) * 16 + j], v[1][2 * j], v[1][2 * j + 1], s);
         }
       }
+      if (!all_lanes(ok && !*abort_flag)) break;   // aborted: nothing is stored
       if (p.split > 1) {
         // this part of the sum, [column][row] over the operand ring: every load into it has
         // been multiplied, and a split CTA takes no further tile
@@ -559,7 +567,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
       }
     }
-  promoted:
     if (lane == 0) bulk_wait_all0();   // this warp's stores have been performed
   }
 
