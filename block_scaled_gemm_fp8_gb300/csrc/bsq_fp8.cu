@@ -94,7 +94,7 @@ struct Fp8Params {
   int32_t raster;              // row tiles of a group
   int32_t split;               // CTAs of a cluster that share a tile's contraction; 1: none
   uint64_t timeout_ns;
-  int32_t drop_announce;       // test hook: the producer never requests a stage's operands
+  int32_t drop_announce;       // test hook: 1, the producer never requests a stage's operands; 2, not a CTA's last ones
 };
 
 struct Fp8Shared {
@@ -367,12 +367,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
     return Tile8{lo, begin + (r0 + l % many) * kRows8, p.offsets ? __ldg(p.offsets + lo) : p.S, (l / many) * BN};
   };
 
+  uint32_t pend_mask = 0, pend_par = 0;   // the producer's: stages it requested, parity of each one's last request
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
       // ===== TMA producer =====
       if (lane == 0) {
-        uint32_t st = 0, sp = 0, pend_mask = 0, pend_par = 0;
+        uint32_t st = 0, sp = 0;
         for (int t = tile0; t < total_tiles && !*abort_flag; t += tile_step) {
           const Tile8 tl = tile_of(t);
           bool ok = true;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!wait8(smem_u32(&sh.empty[st]), sp ^ 1u, abort_flag, p.err, limit)) { ok = false; break; }
             const uint32_t full = smem_u32(&sh.full[st]);
-            if (p.drop_announce) continue;
+            if (p.drop_announce == 1 || (p.drop_announce == 2 && kb == kb1 - 1 && t + tile_step >= total_tiles)) continue;
             mbar_arrive_expect_tx(full, C::kStage);
             const uint32_t dst = smem_u32(smem + st * C::kStage);
             tma_load_2d(dst, &tm_x, full, kb * kDepth, tl.row0);
@@ -399,7 +400,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
           }
           if (!ok) break;
         }
-        if (*abort_flag) drain_pending<C::kStages>(sh.full, pend_mask, pend_par, kDrainLimitNs);
       }
     } else if (warp == 9) {
       // ===== MMA issuer: the whole warp walks the loop, its elected lane issues =====
@@ -607,6 +607,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
   // ---------------------------------------------------------------- teardown
   __syncthreads();
+  // Every role has left.  After an abort copies may be in flight, also when the producer had
+  // ended before it: they land before the CTA's shared memory is another's.
+  if (pend_mask && *abort_flag) drain_pending<C::kStages>(sh.full, pend_mask, pend_par, kDrainLimitNs);
   if (warp == 9 && elected) {   // the lane that issued the MMAs: all of them have completed
     const uint32_t drain = smem_u32(&sh.drain);
     umma_commit(1u, drain);
@@ -670,7 +673,7 @@ int launch_fp8_typed(const Fp8Args& a, const char** msg) {
   p.num_nt = static_cast<int32_t>((outer + BN - 1) / BN);
   p.timeout_ns = wait_limit_ns();
   const char* drop = std::getenv("BSQ_TEST_DROP_ANNOUNCE");
-  p.drop_announce = drop && drop[0] == '1' ? 1 : 0;
+  p.drop_announce = drop && (drop[0] == '1' || drop[0] == '2') ? drop[0] - '0' : 0;
   // an upper bound of the row tiles: the exact count depends on the offsets
   int64_t mt = (a.S + kRows8 - 1) / kRows8;
   if (a.offsets) mt += a.E < a.S ? a.E : a.S;

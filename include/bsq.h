@@ -74,6 +74,9 @@
  *                             MMA thread's wait runs out of time (BSQ_WAIT_LIMIT_*), the kernel
  *                             stops in order and records BSQ_DEVERR_TIMEOUT.  Never set it
  *                             outside such a test: every GEMM and forward call then fails.
+ *                             In the tensor-core kernel of the bsq_fp8_* products 1 = a CTA's
+ *                             operands are never requested, 2 = its last k-block's are not,
+ *                             so that the wait runs out after the requests have ended.
  *       BSQ_TEST_DROP_CHUNK   the same for the small-M kernel (bsq_linear_dgrad with M <= 16,
  *                             decode-sized bsq_grouped_dgrad): every CTA's first chunk is
  *                             never requested, so the wait for it runs out.

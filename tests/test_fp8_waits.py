@@ -40,3 +40,11 @@ def test_loops_are_left_by_a_vote():
             if re.search(r"\bbreak\b", s) or "*abort_flag" in s:
                 assert re.search(r"all_lanes\((ok|!\*abort_flag|ok && !\*abort_flag)\)", s), (name, s)
             assert not re.search(r"\b(if|for|while)\b.*\bok\b", re.sub(r"all_lanes\([^()]*\)", "", s)) or "elected && ok" in s, (name, s)
+
+
+def test_copies_land_after_every_role_has_left():
+    """The producer may have ended when another role's wait runs out: its copies are waited for behind
+    the barrier that all roles reach."""
+    text = open(SOURCE).read()
+    teardown = text[text.index("-- teardown"):]
+    assert "drain_pending" in teardown[teardown.index("__syncthreads()"):teardown.index("tmem_dealloc(")]
