@@ -259,17 +259,25 @@ def _dense(t, dtypes, what):
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
 
 
+def _empty(shape, dtype, like, stream):
+    """A new tensor on `like`'s device for a kernel on `stream`: of that stream's memory, so that no work
+    queued elsewhere still uses it; reused, once freed, after what the current stream does with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def _out(out, shape, dtype, like, stream, what):
-    """`out` checked, or a new tensor on `like`'s device that `stream` may use."""
+    """`out` checked, or a new tensor for `stream`."""
     if out is not None:
         _dense(out, (dtype,), what)
         if out.shape != torch.Size(shape):
             raise ValueError(f"{what}: shape {tuple(out.shape)}, {tuple(shape)} is wanted")
         return out
-    out = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        out.record_stream(stream)
-    return out
+    return _empty(shape, dtype, like, stream)
 
 
 def _raw_stream(stream, like):
