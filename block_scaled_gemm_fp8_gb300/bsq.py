@@ -276,8 +276,18 @@ def _out(out, shape, dtype, like, stream, what):
         _dense(out, (dtype,), what)
         if out.shape != torch.Size(shape):
             raise ValueError(f"{what}: shape {tuple(out.shape)}, {tuple(shape)} is wanted")
+        if out.get_device() != like.get_device():
+            raise ValueError(f"{what}: on {out.device}, the operands are on {like.device}")
         return out
     return _empty(shape, dtype, like, stream)
+
+
+# Index of the current device, without the checks torch.cuda.current_device() makes first.
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
+
+
+def _refuse_device(name, t):
+    raise ValueError(f"{name}: the operands are on {t.device}, kernels are launched on the current device, cuda:{_current_device()}")
 
 
 def _raw_stream(stream, like):
@@ -296,6 +306,8 @@ def quantize_e4m3(x, block_rows=1, codes=None, scale=None, stream=None):
     dtype = _DTYPES.get(x.dtype)
     if dtype is None or not (x.is_cuda and x.is_contiguous()):
         _dense(x, _DTYPES, "quantize_e4m3: x")   # says what is wrong
+    if x.get_device() != _current_device():
+        _refuse_device("quantize_e4m3", x)
     shape = x.shape
     if len(shape) == 3:
         batch, rows, cols = shape
@@ -332,6 +344,8 @@ def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
         raise ValueError(f"{name}: codes {tuple(codes.shape)} on {codes.device}, scale {tuple(scale.shape)} on {scale.device}; "
                          f"[rows, {inner}] and [rows, {blocks}] are wanted; w holds {wd.numel()} codes and {ws.numel()} scales "
                          f"on {wd.device} and {ws.device} for [{batch}, {n}, {k}]")
+    if dev != _current_device():
+        _refuse_device(name, codes)
     if stream is None and out is None:
         out = torch.empty((rows, outer), dtype=torch.bfloat16, device=codes.device)
     else:
@@ -438,6 +452,11 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, seed=0
             raise ValueError("adamw: grad_scale is one number")
     if table.like is None:
         return
+    dev = table.like.get_device()
+    if dev != _current_device():
+        _refuse_device("adamw", table.like)
+    if grad_scale is not None and grad_scale.get_device() != dev:
+        raise ValueError(f"adamw: grad_scale on {grad_scale.device}, the tensors are on {table.like.device}")
     _check(lib().bsq_adamw(table.address, table.count, table.grad_dtype, table.state_bits, step, lr, betas[0], betas[1], eps,
                            None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF,
                            _raw_stream(stream, table.like)))
