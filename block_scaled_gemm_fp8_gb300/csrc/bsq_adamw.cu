@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(kThreadsA<S8>, 1024 / kThreadsA<S8>) adamw_ker
         cv[j / 2] = e4m3x2(round_normal(rj.x, b0 >> 16), round_normal(rj.y, b1 >> 16));
       }
       // Below 2^-6 (2^-15 of the block's largest: rare), or NaN, which only a NaN or infinite
-      // scale leaves: once more in full.
-      if (!(least >= 0.015625f) || !(inv > 0.f)) {
+      // scale of either state leaves (`least` passes over NaN): once more in full.
+      if (!(least >= 0.015625f) || !(im > 0.f) || !(ir > 0.f)) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           float qm[2], qr[2];
