@@ -393,12 +393,34 @@ class _AdamwTensor(ctypes.Structure):
                 ("counter", ctypes.c_uint32)]
 
 
+# Whether tensors[i] still starts at addresses[i], for the given i.
+_at_addresses = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal",
+                        lambda tensors, addresses, which: all(tensors[i].data_ptr() == addresses[i] for i in which))
+
+
 class AdamwTable:
-    """The tensors of an optimizer, checked and laid out once; holds references to them."""
+    """The tensors of an optimizer, checked and laid out once, with the memory they had then.
+
+    Moving or resharding a module gives its parameters other memory (``p.data = ...``), so every step
+    compares the addresses of the parameters and their copies and refuses when one has changed
+    (32 ns each on the GPU's host).  Gradients and states are taken where they were: they are to be
+    written in place, and tensors that replace them (``zero_grad(set_to_none=True)``) need another
+    table.  Their memory is held, whatever their owner does with them."""
 
     def __init__(self, items, grad_dtype, state_bits, keep):
         self.items, self.count, self.grad_dtype, self.state_bits, self.keep = items, len(items), grad_dtype, state_bits, keep
         self.address, self.like = ctypes.addressof(items), keep["params"][0] if keep["params"] else None
+        self.watched = keep["params"] + keep.get("copies", [])
+        self.addresses = [e.param or 0 for e in items] + ([e.copy or 0 for e in items] if "copies" in keep else [])
+        self.places = list(range(len(self.watched)))
+        self.held = [t.untyped_storage() for name, seq in keep.items() if name not in ("params", "copies", "weight_decay") for t in seq]
+
+    def check(self):
+        """Raises when a parameter or a copy is not where the table found it."""
+        if not _at_addresses(self.watched, self.addresses, self.places):
+            i = next(i for i in self.places if self.watched[i].data_ptr() != self.addresses[i])
+            name, i = ("params", i) if i < self.count else ("copies", i - self.count)
+            raise ValueError(f"adamw: {name}[{i}] has other memory than when the table was built; build another one")
 
 
 def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0):
@@ -411,11 +433,11 @@ def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None
     if (v_scales is not None) != s8:
         raise ValueError("adamw_table: m_scales and v_scales come together")
     decays = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
-    lists = dict(params=params, grads=grads, ms=ms, vs=vs, weight_decay=decays)
+    lists = dict(params=list(params), grads=list(grads), ms=list(ms), vs=list(vs), weight_decay=decays)
     if s8:
-        lists.update(m_scales=m_scales, v_scales=v_scales)
+        lists.update(m_scales=list(m_scales), v_scales=list(v_scales))
     if copies is not None:
-        lists.update(copies=copies)
+        lists.update(copies=list(copies))
     for name, seq in lists.items():
         if len(seq) != n:
             raise ValueError(f"adamw_table: {len(seq)} {name} for {n} params")
@@ -426,16 +448,18 @@ def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None
                   m_scales=(torch.float32,), copies=(torch.bfloat16,))
     wanted.update(vs=wanted["ms"], v_scales=wanted["m_scales"])
     items = (_AdamwTensor * n)()
-    counter = 0
+    counter, dev = 0, params[0].get_device() if n else 0
+    columns = [(name, seq, wanted[name], name.endswith("_scales")) for name, seq in lists.items() if name != "weight_decay"]
     for i in range(n):
-        size, blocks = params[i].numel(), -(-params[i].numel() // 128)
-        for name, seq in lists.items():
-            if name == "weight_decay":
-                continue
-            _dense(seq[i], wanted[name], f"adamw_table: {name}[{i}]")
-            if seq[i].numel() != (blocks if name.endswith("_scales") else size) or seq[i].device != params[0].device:
-                raise ValueError(f"adamw_table: {name}[{i}] holds {seq[i].numel()} elements on {seq[i].device}; params[{i}] "
-                                 f"has {size}")
+        size = params[i].numel()
+        blocks = -(-size // 128)
+        for name, seq, dtypes, scales in columns:
+            t = seq[i]
+            if not (t.dtype in dtypes and t.get_device() == dev >= 0 and t.is_contiguous()
+                    and t.numel() == (blocks if scales else size)):
+                _dense(t, dtypes, f"adamw_table: {name}[{i}]")
+                raise ValueError(f"adamw_table: {name}[{i}] holds {t.numel()} elements on {t.device}; params[{i}] has {size} "
+                                 f"and params[0] is on {params[0].device}")
         p = lambda seq: None if seq is None else seq[i].data_ptr()
         items[i] = _AdamwTensor(p(params), p(grads), p(ms), p(vs), p(m_scales), p(v_scales), p(copies), size, decays[i],
                                 counter & 0xFFFFFFFF)
@@ -445,7 +469,8 @@ def adamw_table(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None
 
 def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, seed=0, stream=None):
     """One AdamW step over the tensors of `table`, in place; step counts from 1.  grad_scale: a device
-    float32 that multiplies the gradients (clipping, loss scaling), or None."""
+    float32 that multiplies the gradients (clipping, loss scaling), or None.  step, lr and seed are
+    the call's: a captured graph repeats them."""
     if grad_scale is not None:
         _dense(grad_scale, _F32, "adamw: grad_scale")
         if grad_scale.numel() != 1:
@@ -457,6 +482,7 @@ def adamw(table, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, seed=0
         _refuse_device("adamw", table.like)
     if grad_scale is not None and grad_scale.get_device() != dev:
         raise ValueError(f"adamw: grad_scale on {grad_scale.device}, the tensors are on {table.like.device}")
+    table.check()
     _check(lib().bsq_adamw(table.address, table.count, table.grad_dtype, table.state_bits, step, lr, betas[0], betas[1], eps,
                            None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF,
                            _raw_stream(stream, table.like)))
