@@ -64,9 +64,10 @@ bsq_status device_state(int32_t** err, int* sms) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Shared validation of a packed operand [batch][rows][cols].
+// Shared validation of a packed operand [batch][rows][cols]; block_scale_align: of the 128 x 128
+// blocks' scales, by how the kernels read them.
 bsq_status check_packed(const char* what, int32_t fmt, const void* data, const void* scale, const float* ts,
-                        int64_t batch, int64_t rows, int64_t cols, bool allow_bf16) {
+                        int64_t batch, int64_t rows, int64_t cols, bool allow_bf16, unsigned block_scale_align = 16) {
   if (fmt < BSQ_BF16 || fmt > BSQ_FP8_E5M2_TENSOR) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown format %d", what, fmt);
   if (fmt == BSQ_BF16 && !allow_bf16) return fail(BSQ_ERR_UNSUPPORTED, "%s: BF16 is not a packed format here", what);
   if (batch < 0 || rows < 0 || cols < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
@@ -75,8 +76,8 @@ bsq_status check_packed(const char* what, int32_t fmt, const void* data, const v
   if (elems > 0 && !aligned16(data)) return fail(BSQ_ERR_INVALID_ARG, "%s: data not 16-byte aligned", what);
   if (fmt != BSQ_BF16 && elems > 0 && !scale) return fail(BSQ_ERR_INVALID_ARG, "%s: null scale", what);
   if (fmt == BSQ_NVFP4 && elems > 0 && !ts) return fail(BSQ_ERR_INVALID_ARG, "%s: null tensor_scale", what);
-  if (fmt == BSQ_FP8_E4M3_B128 && elems > 0 && !aligned16(scale))
-    return fail(BSQ_ERR_INVALID_ARG, "%s: scale_inv not 16-byte aligned", what);
+  if (fmt == BSQ_FP8_E4M3_B128 && elems > 0 && (reinterpret_cast<uintptr_t>(scale) & (block_scale_align - 1)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: scale_inv not %u-byte aligned", what, block_scale_align);
   if ((fmt == BSQ_FP8_E4M3_TENSOR || fmt == BSQ_FP8_E5M2_TENSOR) && elems > 0 && (reinterpret_cast<uintptr_t>(scale) & 3u))
     return fail(BSQ_ERR_INVALID_ARG, "%s: scale_inv not 4-byte aligned", what);
   switch (fmt) {
@@ -153,7 +154,8 @@ bsq_status run_fp8(const char* what, bool dgrad, bool grouped, const void* x, co
   if (w_fmt < BSQ_BF16 || w_fmt > BSQ_FP8_E5M2_TENSOR) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown format %d", what, w_fmt);
   if (w_fmt != BSQ_FP8_E4M3_B128)
     return fail(BSQ_ERR_UNSUPPORTED, "%s: W must be E4M3 with a scale per 128 x 128 block", what);
-  bsq_status st = check_packed(what, w_fmt, w, w_scale, nullptr, E, N, K, false);
+  // scales are read one at a time: an expert's slice of a stacked weight starts anywhere
+  bsq_status st = check_packed(what, w_fmt, w, w_scale, nullptr, E, N, K, false, 4);
   if (st != BSQ_OK) return st;
   const int64_t inner = dgrad ? N : K, outer = dgrad ? K : N;
   if (inner % 16) return fail(BSQ_ERR_UNSUPPORTED, "%s: contraction %% 16 != 0 (row pitch must be 16 bytes)", what);

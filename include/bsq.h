@@ -295,8 +295,9 @@ bsq_status bsq_quantize_e4m3(int32_t dtype, const void* x, int64_t batch, int64_
  * Accumulated in FP32 and rounded once to BF16 (the entry points above decode to BF16
  * before they multiply; these multiply the codes).
  * x_codes: u8[M][K], x_scale: f32[M][ceil(K/128)] (bsq_quantize_e4m3, block_rows 1);
- * W: [N][K] in w_fmt, which must be BSQ_FP8_E4M3_B128.  K % 16 == 0, N % 8 == 0; codes, W's
- * scales and y 16-byte aligned, x_scale 4-byte.  y: bf16[M][N], fully written; K == 0 gives zeros.
+ * W: [N][K] in w_fmt, which must be BSQ_FP8_E4M3_B128.  K % 16 == 0, N % 8 == 0; codes
+ * and y 16-byte aligned, scales 4-byte (an expert's slice of a stacked W will do).
+ * y: bf16[M][N], fully written; K == 0 gives zeros.
  * A few rows (M <= 16, or 32 with a small W) take a kernel that streams W into registers.
  */
 bsq_status bsq_fp8_forward(const void* x_codes, const float* x_scale, int64_t M, int32_t w_fmt, const void* w_data,
