@@ -91,25 +91,26 @@ __global__ void __launch_bounds__(kThreadsQ) quantize_e4m3_rows_kernel(const T* 
   const int lane = threadIdx.x & 31;
   const int64_t row = item / segs;
   if (row >= rows) return;
-  const int c0 = static_cast<int>(item - row * segs) * (512 * kChunks) + lane * 16;
+  // unsigned: a row may end within the last piece before 2^31, and that piece past it
+  const uint32_t c0 = static_cast<uint32_t>(item - row * segs) * (512 * kChunks) + lane * 16, end = cols;
   const T* xr = x + row * cols;
   Eight<T> v[kChunks][2];
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (c0 + 512 * i < cols) v[i][h].load(xr + c0 + 512 * i + 8 * h);   // cols % 16 == 0: whole sixteens
+      if (c0 + 512 * i < end) v[i][h].load(xr + c0 + 512 * i + 8 * h);   // cols % 16 == 0: whole sixteens
       else v[i][h].zero();
     }
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int c = c0 + 512 * i;
+    const uint32_t c = c0 + 512 * i;
     uint32_t m = max(v[i][0].amax(), v[i][1].amax());
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float a = block_amax(m);
-    if (c < cols) {
+    if (c < end) {
       const float inv = __fdiv_rn(448.f, a);
       const uint2 lo = encode(v[i][0], inv), hi = encode(v[i][1], inv);
       *reinterpret_cast<uint4*>(codes + row * cols + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
@@ -158,10 +159,10 @@ template <typename T>
 int launch_typed(const QuantE4m3Args& a, const char** msg) {
   const T* x = static_cast<const T*>(a.x);
   uint8_t* codes = static_cast<uint8_t*>(a.codes);
-  const int cols = static_cast<int>(a.cols), nb = (cols + 127) / 128;
+  const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
   int64_t grid;
   if (a.block_rows == 1) {
-    const int segs = (cols + 512 * kChunks - 1) / (512 * kChunks);
+    const int segs = static_cast<int>((a.cols + 512 * kChunks - 1) / (512 * kChunks));
     grid = (a.batch * a.rows * segs + kThreadsQ / 32 - 1) / (kThreadsQ / 32);
     if (grid <= INT32_MAX)
       quantize_e4m3_rows_kernel<T><<<static_cast<unsigned>(grid), kThreadsQ, 0, a.stream>>>(x, a.batch * a.rows, cols, segs, nb,
