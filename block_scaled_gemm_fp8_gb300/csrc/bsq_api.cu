@@ -150,6 +150,9 @@ bsq_status run_fp8(const char* what, bool dgrad, bool grouped, const void* x, co
     if (E > bsq::kMaxExperts) return fail(BSQ_ERR_UNSUPPORTED, "%s: E > %d", what, bsq::kMaxExperts);
     if (!offsets) return fail(BSQ_ERR_INVALID_ARG, "%s: null offsets", what);
     if (!aligned4(offsets)) return fail(BSQ_ERR_INVALID_ARG, "%s: offsets not 4-byte aligned", what);
+    // An expert's rows begin anywhere, so its last tile of 128 may end that far past S; N is rounded
+    // up to blocks of 128.  Both stay below 2^31.
+    if (S > INT32_MAX - 127 || N > INT32_MAX - 127) return fail(BSQ_ERR_UNSUPPORTED, "%s: S or N above 2^31-128", what);
   }
   if (w_fmt < BSQ_BF16 || w_fmt > BSQ_FP8_E5M2_TENSOR) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown format %d", what, w_fmt);
   if (w_fmt != BSQ_FP8_E4M3_B128)

@@ -316,7 +316,7 @@ bsq_status bsq_fp8_dgrad(const void* g_codes, const float* g_scale, int64_t M, i
  * bsq_fp8_grouped_forward, bsq_fp8_grouped_dgrad -- the two products per expert: rows
  * [offsets[e-1] or 0, offsets[e]) against W[e].  W: [E][N][K]; offsets, rows past
  * offsets[E-1] (never written) and the limits on E are those of bsq_grouped_dgrad; an empty
- * contraction is BSQ_ERR_UNSUPPORTED.  A forward of a few rows (S <= 32 and
+ * contraction and an S or N above 2^31 - 128 are BSQ_ERR_UNSUPPORTED.  A forward of a few rows (S <= 32 and
  * S <= 2 E, or S <= 64 and S <= E) takes the few-rows kernel.
  */
 bsq_status bsq_fp8_grouped_forward(const void* x_codes, const float* x_scale, int64_t S, int32_t w_fmt,
