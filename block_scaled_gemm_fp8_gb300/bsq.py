@@ -254,6 +254,8 @@ def grouped_wgrad(grad_out, x, offsets, E, out=None, stream=None):
 
 def _dense(t, dtypes, what):
     """t is a contiguous CUDA tensor of one of `dtypes`."""
+    if t is None:
+        raise ValueError(f"{what}: a CUDA tensor is wanted, not None")
     if not (t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{what}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is wanted, not "
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
@@ -334,7 +336,7 @@ def _fp8(name, codes, scale, w, inner, outer, offsets, out, stream):
     wd, ws, batch, n, k = w.data, w.scale, w.batch, w.rows, w.cols
     dev, rows, blocks = codes.get_device(), codes.shape[0], (inner + 127) // 128
     # one expression for the common case; what is wrong is looked for only when it fails
-    if not (dev >= 0 and scale.get_device() == wd.get_device() == ws.get_device() == dev and codes.dtype in _CODES
+    if not (dev >= 0 and wd is not None and ws is not None and scale.get_device() == wd.get_device() == ws.get_device() == dev and codes.dtype in _CODES
             and wd.dtype in _CODES and scale.dtype is torch.float32 and ws.dtype is torch.float32
             and codes.shape == (rows, inner) and scale.shape == (rows, blocks) and codes.is_contiguous()
             and scale.is_contiguous() and wd.is_contiguous() and ws.is_contiguous() and wd.numel() == batch * n * k
