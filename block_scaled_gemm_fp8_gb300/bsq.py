@@ -123,10 +123,21 @@ def get_device_error(stream=None):
     return st, code.value
 
 
+def _empty(shape, dtype, like, stream):
+    """A new tensor on `like`'s device for a kernel on `stream`: of that stream's memory, so that no work
+    queued elsewhere still uses it; reused, once freed, after what the current stream does with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def dequant(p, out=None, stream=None):
     """BF16 [batch, rows, cols] from a packed operand."""
     if out is None:
-        out = torch.empty((p.batch, p.rows, p.cols), dtype=torch.bfloat16, device=p.data.device)
+        out = _empty((p.batch, p.rows, p.cols), torch.bfloat16, p.data, stream)
     _check(lib().bsq_dequant(p.fmt, _ptr(p.data), _ptr(p.scale), _ptr(p.tensor_scale), p.batch, p.rows, p.cols,
                              _ptr(out), _stream(stream)))
     return out
@@ -136,7 +147,7 @@ def linear_dgrad(grad_out, w, out=None, stream=None):
     """grad_x[M,K] = grad_out[M,N] @ deq(W)[N,K]."""
     M, N = grad_out.shape
     if out is None:
-        out = torch.empty((M, w.cols), dtype=torch.bfloat16, device=grad_out.device)
+        out = _empty((M, w.cols), torch.bfloat16, grad_out, stream)
     _check(lib().bsq_linear_dgrad(_ptr(grad_out), M, N, w.fmt, _ptr(w.data), _ptr(w.scale), _ptr(w.tensor_scale),
                                   w.cols, _ptr(out), _stream(stream)))
     return out
@@ -147,7 +158,7 @@ def linear_dgrad_smallm_noalloc(grad_out, w, out=None, stream=None):
     (split-K scratch in a static device array of the library; K <= 16384)."""
     M, N = grad_out.shape
     if out is None:
-        out = torch.empty((M, w.cols), dtype=torch.bfloat16, device=grad_out.device)
+        out = _empty((M, w.cols), torch.bfloat16, grad_out, stream)
     _check(lib().bsq_linear_dgrad_smallm_noalloc(_ptr(grad_out), M, N, w.fmt, _ptr(w.data), _ptr(w.scale),
                                                  _ptr(w.tensor_scale), w.cols, _ptr(out), _stream(stream)))
     return out
@@ -157,7 +168,7 @@ def linear_wgrad(grad_out, x, out=None, stream=None):
     """grad_w[N,K] = grad_out[M,N]^T @ deq(X)[M,K]."""
     M, N = grad_out.shape
     if out is None:
-        out = torch.empty((N, x.cols), dtype=torch.bfloat16, device=grad_out.device)
+        out = _empty((N, x.cols), torch.bfloat16, grad_out, stream)
     _check(lib().bsq_linear_wgrad(_ptr(grad_out), M, N, x.fmt, _ptr(x.data), _ptr(x.scale), _ptr(x.tensor_scale),
                                   x.cols, _ptr(out), _stream(stream)))
     return out
@@ -170,9 +181,9 @@ def linear_backward(grad_out, w, x, needs=BSQ_NEEDS_GRAD_X | BSQ_NEEDS_GRAD_W, g
     M, N = grad_out.shape
     K = (w if w is not None else x).cols
     if needs & BSQ_NEEDS_GRAD_X and grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=grad_out.device)
+        grad_x = _empty((M, K), torch.bfloat16, grad_out, stream)
     if needs & BSQ_NEEDS_GRAD_W and grad_w is None:
-        grad_w = torch.empty((N, K), dtype=torch.bfloat16, device=grad_out.device)
+        grad_w = _empty((N, K), torch.bfloat16, grad_out, stream)
     f = lambda p, a: None if p is None else getattr(p, a)
     _check(lib().bsq_linear_backward(
         _ptr(grad_out), M, N, f(w, "fmt") or 0, _ptr(f(w, "data")), _ptr(f(w, "scale")), _ptr(f(w, "tensor_scale")),
@@ -185,13 +196,12 @@ def linear_backward(grad_out, w, x, needs=BSQ_NEEDS_GRAD_X | BSQ_NEEDS_GRAD_W, g
 def quantize_e5m2(g, margin=0, codes=None, deq=None, want_deq=True, stream=None):
     """Per-tensor E5M2 quantization of a BF16 gradient with its current amax:
     (codes u8, step f32[1], amax f32[1], deq bf16 or None), all on g's device."""
-    dev = g.device
     if codes is None:
-        codes = torch.empty(g.shape, dtype=torch.uint8, device=dev)
+        codes = _empty(g.shape, torch.uint8, g, stream)
     if deq is None and want_deq:
-        deq = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
-    step = torch.empty(1, dtype=torch.float32, device=dev)
-    amax = torch.empty(1, dtype=torch.float32, device=dev)
+        deq = _empty(g.shape, torch.bfloat16, g, stream)
+    step = _empty(1, torch.float32, g, stream)
+    amax = _empty(1, torch.float32, g, stream)
     _check(lib().bsq_quantize_e5m2(_ptr(g), g.numel(), margin, _ptr(codes), _ptr(deq), _ptr(step), _ptr(amax),
                                    _stream(stream)))
     return codes, step, amax, deq
@@ -203,15 +213,14 @@ def linear_backward_e5m2(grad_out, w, x, needs=BSQ_NEEDS_GRAD_X | BSQ_NEEDS_GRAD
     amax are the quantization's, f32[1] on the device)."""
     M, N = grad_out.shape
     K = (w if w is not None else x).cols
-    dev = grad_out.device
     if needs & BSQ_NEEDS_GRAD_X and grad_x is None:
-        grad_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        grad_x = _empty((M, K), torch.bfloat16, grad_out, stream)
     if needs & BSQ_NEEDS_GRAD_W and grad_w is None:
-        grad_w = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    codes = torch.empty((M, N), dtype=torch.uint8, device=dev)
-    deq = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    step = torch.empty(1, dtype=torch.float32, device=dev)
-    amax = torch.empty(1, dtype=torch.float32, device=dev)
+        grad_w = _empty((N, K), torch.bfloat16, grad_out, stream)
+    codes = _empty((M, N), torch.uint8, grad_out, stream)
+    deq = _empty((M, N), torch.bfloat16, grad_out, stream)
+    step = _empty(1, torch.float32, grad_out, stream)
+    amax = _empty(1, torch.float32, grad_out, stream)
     f = lambda p, a: None if p is None else getattr(p, a)
     _check(lib().bsq_linear_backward_e5m2(
         _ptr(grad_out), M, N, f(w, "fmt") or 0, _ptr(f(w, "data")), _ptr(f(w, "scale")), _ptr(f(w, "tensor_scale")),
@@ -225,7 +234,7 @@ def linear_backward_e5m2(grad_out, w, x, needs=BSQ_NEEDS_GRAD_X | BSQ_NEEDS_GRAD
 def linear_forward(x, w, out=None, stream=None):
     """y[M,N] = deq(X)[M,K] @ deq(W)[N,K]^T; W packed, X packed of W's kind or BF16 (fmt 0)."""
     if out is None:
-        out = torch.empty((x.rows, w.rows), dtype=torch.bfloat16, device=x.data.device)
+        out = _empty((x.rows, w.rows), torch.bfloat16, x.data, stream)
     _check(lib().bsq_linear_forward(x.fmt, _ptr(x.data), _ptr(x.scale), _ptr(x.tensor_scale), x.rows, w.fmt,
                                     _ptr(w.data), _ptr(w.scale), _ptr(w.tensor_scale), w.rows, x.cols, _ptr(out),
                                     _stream(stream)))
@@ -236,7 +245,7 @@ def grouped_dgrad(grad_out, w, offsets, out=None, stream=None):
     """Per expert e: grad_x[r0:r1] = grad_out[r0:r1] @ deq(W[e]); rows past offsets[-1] untouched."""
     S, N = grad_out.shape
     if out is None:
-        out = torch.empty((S, w.cols), dtype=torch.bfloat16, device=grad_out.device)
+        out = _empty((S, w.cols), torch.bfloat16, grad_out, stream)
     _check(lib().bsq_grouped_dgrad(_ptr(grad_out), S, N, w.fmt, _ptr(w.data), _ptr(w.scale), _ptr(w.tensor_scale),
                                    w.batch, w.cols, _ptr(offsets), _ptr(out), _stream(stream)))
     return out
@@ -246,7 +255,7 @@ def grouped_wgrad(grad_out, x, offsets, E, out=None, stream=None):
     """Per expert e: grad_w[e] = grad_out[r0:r1]^T @ deq(X)[r0:r1]; empty experts give zeros."""
     S, N = grad_out.shape
     if out is None:
-        out = torch.empty((E, N, x.cols), dtype=torch.bfloat16, device=grad_out.device)
+        out = _empty((E, N, x.cols), torch.bfloat16, grad_out, stream)
     _check(lib().bsq_grouped_wgrad(_ptr(grad_out), S, N, x.fmt, _ptr(x.data), _ptr(x.scale), _ptr(x.tensor_scale),
                                    x.cols, _ptr(offsets), E, _ptr(out), _stream(stream)))
     return out
@@ -259,17 +268,6 @@ def _dense(t, dtypes, what):
     if not (t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{what}: a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} is wanted, not "
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
-
-
-def _empty(shape, dtype, like, stream):
-    """A new tensor on `like`'s device for a kernel on `stream`: of that stream's memory, so that no work
-    queued elsewhere still uses it; reused, once freed, after what the current stream does with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    t.record_stream(torch.cuda.current_stream(like.device))
-    return t
 
 
 def _out(out, shape, dtype, like, stream, what):

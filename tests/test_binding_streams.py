@@ -84,3 +84,34 @@ def test_outputs_are_the_launching_streams(allocations, name):
     del allocations[:]
     call(None)
     assert allocations and all(a == ("current", []) for a in allocations), allocations
+
+
+def decoding_calls():
+    """The entry points that decode their operands, temporaries of the backward on E5M2 codes included."""
+    g = operand(4, 256, dtype=torch.bfloat16)
+    w = synth.Packed(synth.FMT_FP8, operand(1, 256, 256, dtype=torch.uint8), operand(1, 2, 2), None, 1, 256, 256)
+    x = synth.Packed(synth.FMT_FP8, operand(1, 4, 256, dtype=torch.uint8), operand(1, 1, 2), None, 1, 4, 256)
+    offs = operand(1, dtype=torch.int32)
+    return {
+        "dequant": lambda s: bsq.dequant(w, stream=s),
+        "linear_dgrad": lambda s: bsq.linear_dgrad(g, w, stream=s),
+        "linear_dgrad_smallm_noalloc": lambda s: bsq.linear_dgrad_smallm_noalloc(g, w, stream=s),
+        "linear_wgrad": lambda s: bsq.linear_wgrad(g, x, stream=s),
+        "linear_backward": lambda s: bsq.linear_backward(g, w, x, stream=s),
+        "quantize_e5m2": lambda s: bsq.quantize_e5m2(g, stream=s),
+        "linear_backward_e5m2": lambda s: bsq.linear_backward_e5m2(g, w, x, stream=s),
+        "linear_forward": lambda s: bsq.linear_forward(x, w, stream=s),
+        "grouped_dgrad": lambda s: bsq.grouped_dgrad(g, w, offs, stream=s),
+        "grouped_wgrad": lambda s: bsq.grouped_wgrad(g, x, offs, 1, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", list(decoding_calls()))
+def test_outputs_of_decoding_calls_are_the_launching_streams(allocations, monkeypatch, name):
+    monkeypatch.setattr(bsq, "_stream", lambda stream: 0)
+    call = decoding_calls()[name]
+    call(SIDE)
+    assert allocations and all(a == ("side", ["current"]) for a in allocations), allocations
+    del allocations[:]
+    call(None)
+    assert allocations and all(a == ("current", []) for a in allocations), allocations
