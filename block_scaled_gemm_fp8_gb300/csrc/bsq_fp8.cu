@@ -21,14 +21,17 @@
 //   warps 10-11 scales: xs * ws of each k-block's rows and column halves, into shared memory
 // A 128-deep block of BN = 256 takes 512 tensor-core cycles per SM; its promotion is 64 packed
 // FMAs and 4 TMEM loads per thread, 256 cycles of each SM quarter's FMA pipe.  Measured, M =
-// 8192, N = 14336, K = 5120: 438 us, 2.75 PFLOP/s (1.44 of the measured BF16 burst rate).
-// With parts left out, the same product takes 399 us without output, 385 without the
+// 8192, N = 14336, K = 5120: 480 us as calls on inputs beyond L2, 2.5 PFLOP/s (1.32 of the
+// measured BF16 burst rate); on the same operands 436 over 20 calls back to back, 468 over 400.
+// Over 1 to 16 tiles a CTA and 4 to 64 k-blocks a call takes about 10 us + 1.0 a tile + 0.45 a
+// k-block (within 6 %): the k-block is what counts, and the MMAs alone would take 0.35.
+// With parts left out, 20 calls back to back take 399 us without output, 385 without the
 // promotion's loads and FMAs, 385 without TMA loads, 334 with the MMAs alone and 334 with the
-// promotion alone.  The operands take 48 KB of writes
-// and as many reads of an SM's shared memory a k-block, beside which neither MMAs nor
-// promotion reach their own rate; loading W's tile once for two CTAs (multicast) changed
-// nothing (437 us), so L2 does not bound it.
-// Tried and slower there: CTA pairs of 256 x 256, which halve W's part (509 us, 354 without
+// promotion alone (438 with all of them).  MMAs and promotion share the SM: the operands alone
+// are 48 KB of writes and as many reads of its shared memory a k-block.  Which of the shared
+// parts holds the other up is not settled; loading W's tile once for two CTAs (multicast)
+// changed nothing (437 us), so L2 does not bound it.
+// Tried and slower, back to back: CTA pairs of 256 x 256, which halve W's part (509 us, 354 without
 // promotion: an accumulator's hand-over then crosses SMs; 658 in half accumulators); two
 // 128-column accumulators a k-block with an issuer each (501); 16 promotion warps (513); one
 // scale load per thread in the promotion loop instead of the scale warps (531); scalar FMAs
