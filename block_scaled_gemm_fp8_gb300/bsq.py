@@ -21,8 +21,9 @@ BSQ_BF16, BSQ_FP8_E4M3_B128, BSQ_MXFP4, BSQ_NVFP4, BSQ_FP8_E4M3_TENSOR, BSQ_FP8_
 BSQ_OK, BSQ_ERR_INVALID_ARG, BSQ_ERR_UNSUPPORTED, BSQ_ERR_CUDA, BSQ_ERR_TIMEOUT = 0, 1, 2, 3, 4
 BSQ_NEEDS_GRAD_X, BSQ_NEEDS_GRAD_W = 1, 2
 BSQ_DT_BF16, BSQ_DT_F32 = 0, 1
+BSQ_GATE_SOFTMAX, BSQ_GATE_SIGMOID = 0, 1
 
-_c_void_p, _i64, _i32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double
+_c_void_p, _i64, _i32, _f64, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double, ctypes.c_float
 
 SIGNATURES = {
     "bsq_dequant": [_i32, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p],
@@ -50,6 +51,16 @@ SIGNATURES = {
     "bsq_fp8_grouped_dgrad": [_c_void_p, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
                               _c_void_p, _c_void_p],
     "bsq_adamw": [_c_void_p, _i32, _i32, _i32, _i64, _f64, _f64, _f64, _f64, _c_void_p, ctypes.c_uint32, _c_void_p],
+    "bsq_route": [_i32, _c_void_p, _i64, _i64, _i32, _i32, _i32, _c_void_p, _f32, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_route_backward": [_i32, _c_void_p, _i64, _i64, _i32, _i32, _i32, _f32, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_sort_experts": [_c_void_p, _i64, _i32, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_dispatch": [_c_void_p, _i64, _i64, _c_void_p, _i32, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    "bsq_combine": [_c_void_p, _i64, _i64, _c_void_p, _i32, _c_void_p, _i64, _c_void_p, _c_void_p],
+    "bsq_combine_backward": [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _i32, _c_void_p, _i64, _c_void_p, _c_void_p,
+                             _c_void_p, _c_void_p, _c_void_p],
+    "bsq_fp4_forward": [_c_void_p, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p],
+    "bsq_fp4_grouped_forward": [_c_void_p, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                                _c_void_p, _c_void_p],
     "bsq_status_string": [_i32],
     "bsq_last_error": [],
     "bsq_get_device_error": [ctypes.POINTER(_i32), _c_void_p],
@@ -385,6 +396,235 @@ def fp8_grouped_forward(x_codes, x_scale, w, offsets, out=None, stream=None):
 def fp8_grouped_dgrad(g_codes, g_scale, w, offsets, out=None, stream=None):
     """Per expert e: grad_x[r0:r1] = G[r0:r1] W[e]; rows past offsets[-1] untouched."""
     return _fp8("fp8_grouped_dgrad", g_codes, g_scale, w, w.rows, w.cols, offsets, out, stream)
+
+
+_GATES = {"softmax": BSQ_GATE_SOFTMAX, "sigmoid": BSQ_GATE_SIGMOID}
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _operand(name, t, dtypes, dims, dev):
+    """t is a contiguous CUDA tensor of one of `dtypes` with `dims` dimensions on device `dev`, the current one."""
+    if t is None or not (t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
+        _dense(t, dtypes, name)   # says what is wrong
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, {dims} are wanted")
+    if t.get_device() != dev:
+        if dev == _current_device():
+            raise ValueError(f"{name}: on {t.device}, the operands are on cuda:{dev}")
+        _refuse_device(name, t)
+
+
+def _given(name, t, dtype, shape, dev):
+    """A further operand of a known shape."""
+    if not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+        _dense(t, (dtype,), name)
+        raise ValueError(f"{name}: {tuple(t.shape)} on {t.device}; {tuple(shape)} on cuda:{dev} is wanted")
+
+
+def _first(name, t, dtypes, dims):
+    """The first operand, which says on which device the call is; its device's index."""
+    dev = t.get_device() if t is not None else -1
+    _operand(name, t, dtypes, dims, dev)
+    if dev != _current_device():
+        _refuse_device(name, t)
+    return dev
+
+
+def _new(out, shape, dtype, like, stream, what):
+    """_out with the common case first."""
+    if out is None and stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _out(out, shape, dtype, like, stream, what)
+
+
+def route(logits, k, gate="softmax", renormalize=True, bias=None, factor=1.0, ids=None, weights=None, stream=None):
+    """(ids int32, weights float32), both [T, k]: every token's k experts of the highest logits (BF16 or
+    float32 [T, E]) by falling score, ties to the lowest index, and their weights: factor times the softmax
+    over the chosen logits (renormalize=False: over all), or the sigmoids, divided by their sum
+    (renormalize=False: as they are).  bias (float32 [E]) is added to the logit (sigmoid gate: to its sigmoid) for the
+    choice alone.  A slot that no expert can fill, because logits are minus infinity or NaN, gets id -1 and weight 0."""
+    dev = _first("route", logits, _DTYPES, 2)
+    T, E = logits.shape
+    if gate not in _GATES:
+        raise ValueError(f"route: gate {gate!r}; 'softmax' or 'sigmoid' is wanted")
+    if bias is not None:
+        _given("route: bias", bias, torch.float32, (E,), dev)
+    ids = _new(ids, (T, k), _I32, logits, stream, "route: ids")
+    weights = _new(weights, (T, k), torch.float32, logits, stream, "route: weights")
+    status = (_lib or lib()).bsq_route(_DTYPES[logits.dtype], logits.data_ptr(), T, E, k, _GATES[gate], bool(renormalize),
+                                       None if bias is None else bias.data_ptr(), factor, ids.data_ptr(), weights.data_ptr(),
+                                       _raw_stream(stream, logits))
+    if status:
+        _check(status)
+    return ids, weights
+
+
+def route_backward(logits, ids, grad_weights, gate="softmax", renormalize=True, factor=1.0, out=None, stream=None):
+    """The gradient of `route`'s logits (their type) from that of its weights; gate, renormalize and factor
+    as they were there."""
+    dev = _first("route_backward", logits, _DTYPES, 2)
+    T, E = logits.shape
+    if gate not in _GATES:
+        raise ValueError(f"route_backward: gate {gate!r}; 'softmax' or 'sigmoid' is wanted")
+    _operand("route_backward: ids", ids, (_I32,), 2, dev)
+    k = ids.shape[1]
+    _given("route_backward: ids", ids, _I32, (T, k), dev)
+    _given("route_backward: grad_weights", grad_weights, torch.float32, (T, k), dev)
+    out = _new(out, (T, E), logits.dtype, logits, stream, "route_backward")
+    status = (_lib or lib()).bsq_route_backward(_DTYPES[logits.dtype], logits.data_ptr(), T, E, k, _GATES[gate], bool(renormalize),
+                                                factor, ids.data_ptr(), grad_weights.data_ptr(), out.data_ptr(),
+                                                _raw_stream(stream, logits))
+    if status:
+        _check(status)
+    return out
+
+
+def sort_experts(ids, E, want_slots=True, offsets=None, rows=None, slots=None, stream=None):
+    """(offsets int32 [E], rows int32 [T, k], slots int32 [T * k] or None): where each slot's row is when the slots of
+    ids [T, k] are sorted by expert (stable; -1 for an id outside 0..E-1), the cumulative ends of the experts'
+    rows, and the slot of every row (-1 from the last end on)."""
+    _first("sort_experts", ids, (_I32,), 2)
+    T, k = ids.shape
+    offsets = _new(offsets, (E,), _I32, ids, stream, "sort_experts: offsets")
+    rows = _new(rows, (T, k), _I32, ids, stream, "sort_experts: rows")
+    if want_slots or slots is not None:
+        slots = _new(slots, (T * k,), _I32, ids, stream, "sort_experts: slots")
+    status = (_lib or lib()).bsq_sort_experts(ids.data_ptr(), T, k, E, offsets.data_ptr(), rows.data_ptr(),
+                                              None if slots is None else slots.data_ptr(), _raw_stream(stream, ids))
+    if status:
+        _check(status)
+    return offsets, rows, slots
+
+
+def _written(name, S, cols, bf16, e4m3, out, codes, scale, like, stream):
+    """The rows that dispatch and combine_backward write, and their addresses."""
+    if bf16 or out is not None:
+        out = _new(out, (S, cols), _BF16, like, stream, f"{name}: rows")
+    if e4m3 or codes is not None or scale is not None:
+        codes = _new(codes, (S, cols), torch.uint8, like, stream, f"{name}: codes")
+        scale = _new(scale, (S, (cols + 127) // 128), torch.float32, like, stream, f"{name}: scale")
+    return (out, codes, scale), tuple(None if t is None else t.data_ptr() for t in (out, codes, scale))
+
+
+def dispatch(x, rows, weights=None, S=None, bf16=True, e4m3=False, out=None, codes=None, scale=None, stream=None):
+    """(out, codes, scale): the BF16 tokens x [T, K] at their rows, out[rows[t, j]] = weights[t, j] * x[t] (weights float32
+    [T, k], or None for 1), as BF16 rows [S, K], as E4M3 codes [S, K] with scales [S, ceil(K / 128)] (quantize_e4m3's
+    of the token, the scales times the weight), or both; None for what is not wanted.  S: rows in all, as many as
+    there are slots if not given.  Rows that no slot owns are not written."""
+    dev = _first("dispatch", x, (_BF16,), 2)
+    T, K = x.shape
+    _operand("dispatch: rows", rows, (_I32,), 2, dev)
+    k = rows.shape[1]
+    _given("dispatch: rows", rows, _I32, (T, k), dev)
+    if weights is not None:
+        _given("dispatch: weights", weights, torch.float32, (T, k), dev)
+    if S is None:
+        S = next((t.shape[0] for t in (out, codes, scale) if t is not None), T * k)
+    if not (bf16 or e4m3 or out is not None or codes is not None or scale is not None):
+        raise ValueError("dispatch: neither BF16 rows nor E4M3 codes are wanted")
+    made, at = _written("dispatch", S, K, bf16, e4m3, out, codes, scale, x, stream)
+    status = (_lib or lib()).bsq_dispatch(x.data_ptr(), T, K, rows.data_ptr(), k, None if weights is None else weights.data_ptr(), S,
+                                          *at, _raw_stream(stream, x))
+    if status:
+        _check(status)
+    return made
+
+
+def combine(y, rows, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * y[rows[t, j]] (BF16 [T, N]) of the BF16 rows y [S, N]; weights float32 [T, k], or None
+    for 1.  A row outside y adds nothing.  Also the gradient of dispatch's x, from that of its rows."""
+    dev = _first("combine", y, (_BF16,), 2)
+    S, N = y.shape
+    _operand("combine: rows", rows, (_I32,), 2, dev)
+    T, k = rows.shape
+    if weights is not None:
+        _given("combine: weights", weights, torch.float32, (T, k), dev)
+    out = _new(out, (T, N), _BF16, y, stream, "combine")
+    status = (_lib or lib()).bsq_combine(y.data_ptr(), S, N, rows.data_ptr(), k, None if weights is None else weights.data_ptr(), T,
+                                         out.data_ptr(), _raw_stream(stream, y))
+    if status:
+        _check(status)
+    return out
+
+
+def combine_backward(grad_out, y, rows, weights=None, bf16=True, e4m3=False, want_weights=True, S=None, grad_y=None, codes=None,
+                     scale=None, grad_weights=None, stream=None):
+    """(grad_y, codes, scale, grad_weights) of combine from grad_out [T, N]: weights[t, j] * grad_out[t] at each row, as BF16
+    and E4M3 rows as dispatch writes them, and grad_out[t] . y[rows[t, j]] (float32 [T, k]); None for what is not wanted.
+    y may be None without want_weights; then S rows are written, as many as there are slots if not given."""
+    dev = _first("combine_backward", grad_out, (_BF16,), 2)
+    T, N = grad_out.shape
+    _operand("combine_backward: rows", rows, (_I32,), 2, dev)
+    k = rows.shape[1]
+    _given("combine_backward: rows", rows, _I32, (T, k), dev)
+    if weights is not None:
+        _given("combine_backward: weights", weights, torch.float32, (T, k), dev)
+    if y is not None:
+        _operand("combine_backward: y", y, (_BF16,), 2, dev)
+        if y.shape[1] != N or S not in (None, y.shape[0]):
+            raise ValueError(f"combine_backward: y {tuple(y.shape)}; {'any' if S is None else S} rows of {N} are wanted")
+        S = y.shape[0]
+    elif want_weights or grad_weights is not None:
+        raise ValueError("combine_backward: the gradient of the weights needs y")
+    if S is None:
+        S = next((t.shape[0] for t in (grad_y, codes, scale) if t is not None), T * k)
+    made, at = _written("combine_backward", S, N, bf16, e4m3, grad_y, codes, scale, grad_out, stream)
+    if want_weights or grad_weights is not None:
+        grad_weights = _new(grad_weights, (T, k), torch.float32, grad_out, stream, "combine_backward: grad_weights")
+    status = (_lib or lib()).bsq_combine_backward(
+        grad_out.data_ptr(), None if y is None else y.data_ptr(), S, N, rows.data_ptr(), k,
+        None if weights is None else weights.data_ptr(), T, *at, None if grad_weights is None else grad_weights.data_ptr(),
+        _raw_stream(stream, grad_out))
+    if status:
+        _check(status)
+    return (*made, grad_weights)
+
+
+def _fp4(name, x, w, offsets, out, stream):
+    dev = _first(name, x, (_BF16,), 2)
+    rows, k = x.shape
+    wd, ws, ts, batch, n = w.data, w.scale, w.tensor_scale, w.batch, w.rows
+    group = 16 if w.fmt == BSQ_NVFP4 else 32
+    # one expression for the common case; what is wrong is looked for only when it fails
+    if not (wd is not None and ws is not None and wd.dtype is torch.uint8 and wd.get_device() == ws.get_device() == dev
+            and (ws.dtype is torch.uint8 or ws.dtype is torch.float8_e4m3fn) and wd.is_contiguous() and ws.is_contiguous()
+            and k == w.cols and (w.fmt not in (BSQ_MXFP4, BSQ_NVFP4) or (2 * wd.numel() == batch * n * k and ws.numel() * group == batch * n * k))
+            and (w.fmt != BSQ_NVFP4 or (ts is not None and ts.dtype is torch.float32 and ts.get_device() == dev
+                                        and ts.is_contiguous() and ts.numel() == batch))):
+        for t, dtypes, what in ((wd, (torch.uint8,), "w.data"), (ws, (torch.uint8, torch.float8_e4m3fn), "w.scale")):
+            _dense(t, dtypes, f"{name}: {what}")
+        if w.fmt == BSQ_NVFP4:
+            _dense(ts, _F32, f"{name}: w.tensor_scale")
+        raise ValueError(f"{name}: x {tuple(x.shape)} on {x.device}; w [{batch}, {n}, {w.cols}] holds {wd.numel()} bytes of codes and "
+                         f"{ws.numel()} scales on {wd.device} and {ws.device}, {'no tensor scales' if ts is None else f'{ts.numel()} tensor scales on {ts.device}'}")
+    if offsets is None:
+        if batch != 1:
+            raise ValueError(f"{name}: one weight is wanted, not {batch}")
+    else:
+        _dense(offsets, (_I32,), name)
+        if offsets.numel() != batch or offsets.get_device() != dev:
+            raise ValueError(f"{name}: {offsets.numel()} offsets on {offsets.device} for {batch} experts")
+    out = _new(out, (rows, n), _BF16, x, stream, name)
+    ts = None if ts is None else ts.data_ptr()
+    raw = _raw_stream(stream, x)
+    if offsets is None:
+        status = (_lib or lib()).bsq_fp4_forward(x.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), ts, n, k, out.data_ptr(), raw)
+    else:
+        status = (_lib or lib()).bsq_fp4_grouped_forward(x.data_ptr(), rows, w.fmt, wd.data_ptr(), ws.data_ptr(), ts, batch, n, k,
+                                                         offsets.data_ptr(), out.data_ptr(), raw)
+    if status:
+        _check(status)
+    return out
+
+
+def fp4_forward(x, w, out=None, stream=None):
+    """y[M,N] (BF16) = X[M,K] deq(W)[N,K]^T of a BF16 X and a W in MXFP4 or NVFP4: for few rows (decoding)."""
+    return _fp4("fp4_forward", x, w, None, out, stream)
+
+
+def fp4_grouped_forward(x, w, offsets, out=None, stream=None):
+    """Per expert e: y[r0:r1] = X[r0:r1] deq(W[e])^T; rows past offsets[-1] untouched."""
+    return _fp4("fp4_grouped_forward", x, w, offsets, out, stream)
 
 
 class _AdamwTensor(ctypes.Structure):

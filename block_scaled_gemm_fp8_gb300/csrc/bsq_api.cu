@@ -11,6 +11,7 @@
 
 #include "bsq_fp8_internal.h"
 #include "bsq_internal.h"
+#include "bsq_moe_internal.h"
 #include "../../include/bsq.h"
 
 namespace {
@@ -182,6 +183,82 @@ bsq_status run_fp8(const char* what, bool dgrad, bool grouped, const void* x, co
   const char* msg = "";
   if ((bsq::fp8_takes_smallm(a) ? bsq::launch_fp8_smallm(a, &msg) : bsq::launch_fp8(a, &msg)) != 0)
     return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+// Rows, weights and sizes that the operators between tokens [T][cols] and rows [S][cols] share.
+bsq_status check_tokens(const char* what, int64_t T, int64_t S, int64_t cols, const int32_t* rows, int32_t k,
+                        const float* weights) {
+  if (T < 0 || S < 0 || cols < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (T > INT32_MAX || S > INT32_MAX || cols > INT32_MAX) return fail(BSQ_ERR_UNSUPPORTED, "%s: size above 2^31-1", what);
+  if (k < 1) return fail(BSQ_ERR_INVALID_ARG, "%s: k must be >= 1", what);
+  if (k > bsq::kMaxSlots) return fail(BSQ_ERR_UNSUPPORTED, "%s: k > %d", what, bsq::kMaxSlots);
+  if (cols % 8) return fail(BSQ_ERR_UNSUPPORTED, "%s: columns %% 8 != 0 (row pitch must be 16 bytes)", what);
+  if (T > 0 && (!rows || !aligned4(rows))) return fail(BSQ_ERR_INVALID_ARG, "%s: rows null or not 4-byte aligned", what);
+  if (!aligned4(weights)) return fail(BSQ_ERR_INVALID_ARG, "%s: weights not 4-byte aligned", what);
+  return BSQ_OK;
+}
+
+// The rows that bsq_dispatch and bsq_combine_backward write: BF16, E4M3 codes with scales, or both.
+bsq_status check_written(const char* what, int64_t S, int64_t cols, const void* out, const void* codes, const float* scale) {
+  if (!codes != !scale) return fail(BSQ_ERR_INVALID_ARG, "%s: codes and scale come together", what);
+  if (codes && cols % 16) return fail(BSQ_ERR_UNSUPPORTED, "%s: codes of columns %% 16 != 0 (row pitch must be 16 bytes)", what);
+  if (!aligned16(out) || !aligned16(codes)) return fail(BSQ_ERR_INVALID_ARG, "%s: output not 16-byte aligned", what);
+  if (!aligned4(scale)) return fail(BSQ_ERR_INVALID_ARG, "%s: scale not 4-byte aligned", what);
+  return BSQ_OK;
+}
+
+bsq_status check_route(const char* what, int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate,
+                       float factor) {
+  if (dtype != BSQ_DT_BF16 && dtype != BSQ_DT_F32) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown type %d", what, dtype);
+  if (gate != BSQ_GATE_SOFTMAX && gate != BSQ_GATE_SIGMOID) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown gate %d", what, gate);
+  if (T < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (E < 1 || k < 1 || k > E) return fail(BSQ_ERR_INVALID_ARG, "%s: k = %d of E = %lld experts", what, k, static_cast<long long>(E));
+  if (E > bsq::kMaxExperts || k > bsq::kMaxSlots || T > INT32_MAX)
+    return fail(BSQ_ERR_UNSUPPORTED, "%s: E > %d, k > %d or T above 2^31-1", what, bsq::kMaxExperts, bsq::kMaxSlots);
+  if (!std::isfinite(factor)) return fail(BSQ_ERR_INVALID_ARG, "%s: factor must be finite", what);
+  const uintptr_t mask = dtype == BSQ_DT_BF16 ? 1u : 3u;
+  if (T > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & mask)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: logits null or not aligned to their elements", what);
+  return BSQ_OK;
+}
+
+// The forward of a BF16 X and a 4-bit W.
+bsq_status run_fp4(const char* what, bool grouped, const void* x, int64_t S, int32_t w_fmt, const void* w, const void* w_scale,
+                   const float* ts, int64_t E, int64_t N, int64_t K, const int32_t* offsets, void* y, void* stream) {
+  if (S < 0 || N < 0 || K < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (S > INT32_MAX - 127 || N > INT32_MAX - 127) return fail(BSQ_ERR_UNSUPPORTED, "%s: S or N above 2^31-128", what);
+  if (K > (1 << 24)) return fail(BSQ_ERR_UNSUPPORTED, "%s: K above 2^24", what);
+  if (grouped) {
+    if (E < 1) return fail(BSQ_ERR_INVALID_ARG, "%s: E must be >= 1", what);
+    if (E > bsq::kMaxExperts) return fail(BSQ_ERR_UNSUPPORTED, "%s: E > %d", what, bsq::kMaxExperts);
+    if (!offsets) return fail(BSQ_ERR_INVALID_ARG, "%s: null offsets", what);
+    if (!aligned4(offsets)) return fail(BSQ_ERR_INVALID_ARG, "%s: offsets not 4-byte aligned", what);
+  }
+  if (w_fmt < BSQ_BF16 || w_fmt > BSQ_FP8_E5M2_TENSOR) return fail(BSQ_ERR_INVALID_ARG, "%s: unknown format %d", what, w_fmt);
+  if (w_fmt != BSQ_MXFP4 && w_fmt != BSQ_NVFP4) return fail(BSQ_ERR_UNSUPPORTED, "%s: W must be MXFP4 or NVFP4", what);
+  bsq_status st = check_packed(what, w_fmt, w, w_scale, ts, E, N, K, false);
+  if (st != BSQ_OK) return st;
+  if (K % 32) return fail(BSQ_ERR_UNSUPPORTED, "%s: K %% 32 != 0 (packed row pitch must be 16 bytes)", what);
+  if (N % 8) return fail(BSQ_ERR_UNSUPPORTED, "%s: N %% 8 != 0 (Y row pitch must be 16 bytes)", what);
+  if (E * N * K > 0 && ((reinterpret_cast<uintptr_t>(w_scale) & 1u) || !aligned4(ts)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: scale not 2-byte or tensor_scale not 4-byte aligned", what);
+  if (S * K > 0 && (!x || !aligned16(x))) return fail(BSQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", what);
+  if (S * N > 0 && (!y || !aligned16(y))) return fail(BSQ_ERR_INVALID_ARG, "%s: output null or not 16-byte aligned", what);
+  if (S == 0 || N == 0) return BSQ_OK;
+  if (K == 0) {
+    if (grouped) return fail(BSQ_ERR_UNSUPPORTED, "%s: K == 0 with S > 0 (rows to zero depend on offsets)", what);
+    return zero_output(y, S * N * 2, static_cast<cudaStream_t>(stream), what);
+  }
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::Fp4Args a{w_fmt, x, w, w_scale, ts, S, N, K, E, grouped ? offsets : nullptr, y, err, sms, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (!grouped && !bsq::fp4_takes_smallm(a))
+    return bsq_linear_forward(BSQ_BF16, x, nullptr, nullptr, S, w_fmt, w, w_scale, ts, N, K, y, stream);
+  if (bsq::launch_fp4_smallm(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
   return BSQ_OK;
 }
 
@@ -588,6 +665,141 @@ bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, int32_t gra
   const char* msg = "";
   if (bsq::launch_adamw(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
   return BSQ_OK;
+}
+
+bsq_status bsq_route(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate, int32_t renormalize,
+                     const float* bias, float factor, int32_t* ids, float* weights, void* stream) {
+  const char* what = "bsq_route";
+  bsq_status st = check_route(what, dtype, logits, T, E, k, gate, factor);
+  if (st != BSQ_OK) return st;
+  if (T > 0 && (!ids || !weights)) return fail(BSQ_ERR_INVALID_ARG, "%s: null output", what);
+  if (!aligned4(bias) || !aligned4(ids) || !aligned4(weights))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: bias, ids or weights not 4-byte aligned", what);
+  if (T == 0) return BSQ_OK;
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::RouteArgs a{dtype, logits, T, static_cast<int>(E), k, gate, renormalize != 0, bias, factor, ids, weights, nullptr, nullptr,
+                   static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_route(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_route_backward(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate,
+                              int32_t renormalize, float factor, const int32_t* ids, const float* grad_weights,
+                              void* grad_logits, void* stream) {
+  const char* what = "bsq_route_backward";
+  bsq_status st = check_route(what, dtype, logits, T, E, k, gate, factor);
+  if (st != BSQ_OK) return st;
+  const uintptr_t mask = dtype == BSQ_DT_BF16 ? 1u : 3u;
+  if (T > 0 && (!ids || !grad_weights || !grad_logits)) return fail(BSQ_ERR_INVALID_ARG, "%s: null ids, grad_weights or grad_logits", what);
+  if (!aligned4(ids) || !aligned4(grad_weights) || (reinterpret_cast<uintptr_t>(grad_logits) & mask))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: a pointer is not aligned to its elements", what);
+  if (T == 0) return BSQ_OK;
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::RouteArgs a{dtype, logits, T, static_cast<int>(E), k, gate, renormalize != 0, nullptr, factor, const_cast<int32_t*>(ids), nullptr,
+                   grad_weights, grad_logits, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_route_backward(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_sort_experts(const int32_t* ids, int64_t T, int32_t k, int64_t E, int32_t* offsets, int32_t* rows,
+                            int32_t* slots, void* stream) {
+  const char* what = "bsq_sort_experts";
+  if (T < 0) return fail(BSQ_ERR_INVALID_ARG, "%s: negative size", what);
+  if (E < 1 || k < 1) return fail(BSQ_ERR_INVALID_ARG, "%s: E and k must be >= 1", what);
+  if (E > bsq::kMaxExperts || k > bsq::kMaxSlots)
+    return fail(BSQ_ERR_UNSUPPORTED, "%s: E > %d or k > %d", what, bsq::kMaxExperts, bsq::kMaxSlots);
+  if (T > INT32_MAX / k) return fail(BSQ_ERR_UNSUPPORTED, "%s: T * k above 2^31-1", what);
+  if (!offsets || (T > 0 && (!ids || !rows))) return fail(BSQ_ERR_INVALID_ARG, "%s: null ids, offsets or rows", what);
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(rows) || !aligned4(slots))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: a pointer is not 4-byte aligned", what);
+  int32_t* err = nullptr;
+  int sms = 0;
+  const bsq_status st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::SortArgs a{ids, T * k, static_cast<int>(E), offsets, rows, slots, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_sort_experts(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_dispatch(const void* x, int64_t T, int64_t K, const int32_t* rows, int32_t k, const float* weights, int64_t S,
+                        void* out, void* codes, float* scale, void* stream) {
+  const char* what = "bsq_dispatch";
+  bsq_status st = check_tokens(what, T, S, K, rows, k, weights);
+  if (st == BSQ_OK) st = check_written(what, S, K, out, codes, scale);
+  if (st != BSQ_OK) return st;
+  if (T * K > 0 && (!x || !aligned16(x))) return fail(BSQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", what);
+  if (T == 0 || K == 0 || S == 0) return BSQ_OK;
+  if (!out && !codes) return fail(BSQ_ERR_INVALID_ARG, "%s: neither out nor codes", what);
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::TokenArgs a{x, nullptr, T, S, K, rows, k, weights, out, codes, scale, nullptr, sms, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_dispatch(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_combine(const void* y, int64_t S, int64_t N, const int32_t* rows, int32_t k, const float* weights, int64_t T,
+                       void* out, void* stream) {
+  const char* what = "bsq_combine";
+  bsq_status st = check_tokens(what, T, S, N, rows, k, weights);
+  if (st != BSQ_OK) return st;
+  if (S * N > 0 && (!y || !aligned16(y))) return fail(BSQ_ERR_INVALID_ARG, "%s: y null or not 16-byte aligned", what);
+  if (T * N > 0 && (!out || !aligned16(out))) return fail(BSQ_ERR_INVALID_ARG, "%s: output null or not 16-byte aligned", what);
+  if (T == 0 || N == 0) return BSQ_OK;
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::TokenArgs a{nullptr, y, T, S, N, rows, k, weights, out, nullptr, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_combine(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_combine_backward(const void* grad_out, const void* y, int64_t S, int64_t N, const int32_t* rows, int32_t k,
+                                const float* weights, int64_t T, void* grad_y, void* codes, float* scale, float* grad_weights,
+                                void* stream) {
+  const char* what = "bsq_combine_backward";
+  bsq_status st = check_tokens(what, T, S, N, rows, k, weights);
+  if (st == BSQ_OK) st = check_written(what, S, N, grad_y, codes, scale);
+  if (st != BSQ_OK) return st;
+  if (T * N > 0 && (!grad_out || !aligned16(grad_out)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: grad_out null or not 16-byte aligned", what);
+  if (grad_weights && T > 0 && S * N > 0 && (!y || !aligned16(y)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: grad_weights needs y, 16-byte aligned", what);
+  if (!aligned4(grad_weights)) return fail(BSQ_ERR_INVALID_ARG, "%s: grad_weights not 4-byte aligned", what);
+  if (T == 0 || (!grad_y && !codes && !grad_weights)) return BSQ_OK;
+  if (N == 0 || S == 0) return grad_weights ? zero_output(grad_weights, T * k * 4, static_cast<cudaStream_t>(stream), what) : BSQ_OK;
+  int32_t* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != BSQ_OK) return st;
+  bsq::TokenArgs a{grad_out, y, T, S, N, rows, k, weights, grad_y, codes, scale, grad_weights, sms, static_cast<cudaStream_t>(stream)};
+  const char* msg = "";
+  if (bsq::launch_combine_backward(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  return BSQ_OK;
+}
+
+bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* w_data, const void* w_scale,
+                           const float* w_tensor_scale, int64_t N, int64_t K, void* y, void* stream) {
+  return run_fp4("bsq_fp4_forward", false, x, M, w_fmt, w_data, w_scale, w_tensor_scale, 1, N, K, nullptr, y, stream);
+}
+
+bsq_status bsq_fp4_grouped_forward(const void* x, int64_t S, int32_t w_fmt, const void* w_data, const void* w_scale,
+                                   const float* w_tensor_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
+                                   void* y, void* stream) {
+  return run_fp4("bsq_fp4_grouped_forward", true, x, S, w_fmt, w_data, w_scale, w_tensor_scale, E, N, K, offsets, y, stream);
 }
 
 }  // extern "C"

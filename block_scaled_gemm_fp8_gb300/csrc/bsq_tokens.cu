@@ -1,0 +1,431 @@
+// bsq_tokens.cu -- tokens to their experts' rows and back.
+//
+//   sort      rows[i] = place of slot i (token i / k) when slots are sorted by expert, stable
+//   dispatch  out[rows[t, j]] = w[t, j] x[t], as BF16 and as E4M3 codes of x[t] in blocks of 128
+//             columns with the blocks' scales times w[t, j]
+//   combine   out[t] = sum_j w[t, j] y[rows[t, j]], in the order of j, float32, rounded once
+//   backward  grad_y[rows[t, j]] = w[t, j] g[t] (as dispatch), grad_w[t, j] = g[t] . y[rows[t, j]]
+//
+// All but the sort are bound by HBM: a token's columns are read once, whatever k is, and a
+// token's codes are made once, since a weight only changes a block's scale.
+#include <cuda_bf16.h>
+
+#include "bsq_e4m3.cuh"
+#include "bsq_moe_internal.h"
+#include "bsq_ptx.cuh"
+#include "../../include/bsq.h"
+
+namespace bsq {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+int last_error(const char** msg) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return 0;
+  *msg = cudaGetErrorString(e);
+  return static_cast<int>(e);
+}
+
+// ---------------------------------------------------------------- sort
+constexpr int kSortWarps = 32;
+constexpr int kAheadS = 4;       // ids a lane loads before the first is counted
+
+// A counting sort in one launch of one cluster.  Every warp counts its run of slots in
+// counters of its own (lanes of one expert find one another by match, so nothing is
+// added atomically), the counts become first places (over warps, CTAs through
+// distributed shared memory, then experts), and every warp goes over its run again.
+__global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
+                                                                      int64_t run, int ctas, int32_t* __restrict__ offsets,
+                                                                      int32_t* __restrict__ rows, int32_t* __restrict__ slots) {
+  extern __shared__ int32_t counts[];      // [kSortWarps][E], total[E], base[E]
+  int32_t* total = counts + kSortWarps * E;
+  int32_t* base = total + E;
+  __shared__ int32_t wsum[kSortWarps];
+  __shared__ int32_t kept;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.x);
+  for (int i = tid; i < kSortWarps * E; i += kSortWarps * 32) counts[i] = 0;
+  __syncthreads();
+  int32_t* mine = counts + warp * E;
+  const int64_t begin = min(n, (static_cast<int64_t>(rank) * kSortWarps + warp) * run), end = min(n, begin + run);
+  const uint32_t below = (1u << lane) - 1u;
+
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
+    int e[kAheadS];
+#pragma unroll
+    for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < kAheadS; ++u) {
+      const bool in = static_cast<unsigned>(e[u]) < static_cast<unsigned>(E);
+      const uint32_t same = __match_any_sync(kFull, in ? e[u] : -1);
+      if (in && (same & below) == 0) mine[e[u]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  int32_t sum = 0;                          // thread e: slots of expert e in this CTA
+  if (tid < E) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = counts[w * E + tid];
+      counts[w * E + tid] = sum;
+      sum += c;
+    }
+    total[tid] = sum;
+  }
+  int32_t before = 0, all = sum;
+  if (ctas > 1) {
+    cluster_sync();
+    if (tid < E) {
+      all = 0;
+      for (int c = 0; c < ctas; ++c) {
+        const int32_t v = static_cast<int32_t>(ld_shared_cluster_u32(map_to_rank(smem_u32(total + tid), c)));
+        before += c < rank ? v : 0;
+        all += v;
+      }
+    }
+  }
+  int32_t upto = tid < E ? all : 0;         // inclusive sum over experts (E <= 1024, one a thread)
+  const int32_t own = upto;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t v = __shfl_up_sync(kFull, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) wsum[warp] = upto;
+  __syncthreads();
+  int32_t ahead = lane < warp ? wsum[lane] : 0;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) ahead += __shfl_xor_sync(kFull, ahead, d);
+  upto += ahead;
+  if (tid < E) {
+    base[tid] = upto - own + before;
+    if (rank == 0) offsets[tid] = upto;
+    if (tid == E - 1) kept = upto;
+  }
+  // the cluster's counts have been read: no CTA leaves before
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+
+  if (slots)
+    for (int64_t i = static_cast<int64_t>(kept) + rank * (kSortWarps * 32) + tid; i < n; i += static_cast<int64_t>(ctas) * (kSortWarps * 32))
+      slots[i] = -1;
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
+    int e[kAheadS];
+#pragma unroll
+    for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < kAheadS; ++u) {
+      const bool in = static_cast<unsigned>(e[u]) < static_cast<unsigned>(E);
+      const uint32_t same = __match_any_sync(kFull, in ? e[u] : -1);
+      const int64_t i = i0 + 32 * u + lane;
+      int32_t place = -1;
+      if (in) place = base[e[u]] + mine[e[u]] + __popc(same & below);
+      __syncwarp();
+      if (in && (same & below) == 0) mine[e[u]] += __popc(same);
+      __syncwarp();
+      if (i < end) rows[i] = place;
+      if (in && slots) slots[place] = static_cast<int32_t>(i);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows of a token
+// Lane j < k holds slot j's row (-1: none) and weight.
+struct Slots {
+  int32_t row;
+  float weight;
+  __device__ Slots(const int32_t* rows, const float* weights, int64_t t, int k, int64_t S, int lane) {
+    row = lane < k ? __ldg(rows + t * k + lane) : -1;
+    if (row >= S) row = -1;
+    weight = weights && lane < k ? __ldg(weights + t * k + lane) : 1.f;
+  }
+};
+
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t v, float w) {
+  return pack_bf16x2(__float_as_uint(__uint_as_float(v << 16) * w), __float_as_uint(__uint_as_float(v & 0xFFFF0000u) * w));
+}
+__device__ __forceinline__ uint4 scaled(const uint4& v, float w) {
+  return make_uint4(scaled_pair(v.x, w), scaled_pair(v.y, w), scaled_pair(v.z, w), scaled_pair(v.w, w));
+}
+// Largest magnitude of the 128-column block that 16 lanes of eight columns hold.
+__device__ __forceinline__ float block_amax16(const Eight<__nv_bfloat16>& v) {
+  uint32_t m = v.amax();
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
+  return block_amax(m);
+}
+
+constexpr int kThreadsT = 256;
+constexpr int kPieces = 2;       // pieces of 256 columns (eight a lane) per warp
+
+template <bool BF16, bool E4M3>
+__global__ void __launch_bounds__(kThreadsT) dispatch_kernel(const __nv_bfloat16* __restrict__ x, int64_t tokens, int64_t S,
+                                                            int cols, int segs, int nblocks, const int32_t* __restrict__ rows,
+                                                            int k, const float* __restrict__ weights,
+                                                            __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ codes,
+                                                            float* __restrict__ scale) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreadsT / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = item / segs;
+  if (t >= tokens) return;
+  const Slots s(rows, weights, t, k, S, lane);
+  // unsigned: a token may end within the last piece before 2^31
+  const uint32_t c0 = static_cast<uint32_t>(item - t * segs) * (256 * kPieces) + lane * 8, end = cols;
+  Eight<__nv_bfloat16> v[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if (c0 + 256 * i < end) v[i].load(x + t * cols + c0 + 256 * i);
+    else v[i].zero();
+  }
+  float sc[kPieces];
+  uint2 code[kPieces];
+  if (E4M3) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const float a = block_amax16(v[i]);
+      code[i] = encode(v[i], __fdiv_rn(448.f, a));
+      sc[i] = __fdiv_rn(a, 448.f);
+    }
+  }
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = __shfl_sync(kFull, s.row, j);
+    const float w = __shfl_sync(kFull, s.weight, j);
+    if (r < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t c = c0 + 256 * i;
+      if (c >= end) continue;
+      if (BF16) *reinterpret_cast<uint4*>(out + r * cols + c) = weights ? scaled(v[i].v, w) : v[i].v;
+      if (E4M3) {
+        *reinterpret_cast<uint2*>(codes + r * cols + c) = code[i];
+        if ((lane & 15) == 0) scale[r * nblocks + (c >> 7)] = sc[i] * w;
+      }
+    }
+  }
+}
+
+// Slots whose rows are in flight together.
+constexpr int kTogether = 4;
+
+__global__ void __launch_bounds__(kThreadsT) combine_kernel(const __nv_bfloat16* __restrict__ y, int64_t tokens, int64_t S,
+                                                           int cols, int segs, const int32_t* __restrict__ rows, int k,
+                                                           const float* __restrict__ weights, __nv_bfloat16* __restrict__ out) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreadsT / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = item / segs;
+  if (t >= tokens) return;
+  const Slots s(rows, weights, t, k, S, lane);
+  const uint32_t c = static_cast<uint32_t>(item - t * segs) * 256 + lane * 8;
+  const bool in = c < static_cast<uint32_t>(cols);
+  float acc[8] = {};
+  for (int j0 = 0; j0 < k; j0 += kTogether) {
+    Eight<__nv_bfloat16> v[kTogether];
+    float w[kTogether];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) {
+      const int64_t r = __shfl_sync(kFull, s.row, j0 + u);     // j0 + u < 32; lanes from k on hold -1
+      w[u] = __shfl_sync(kFull, s.weight, j0 + u);
+      if (r < 0) w[u] = 0.f;
+      if (r >= 0 && in) v[u].load(y + r * cols + c);
+      else v[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = v[u].pair(i);
+        acc[2 * i] = fmaf(w[u], f.x, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w[u], f.y, acc[2 * i + 1]);
+      }
+  }
+  if (!in) return;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(__float_as_uint(acc[2 * i]), __float_as_uint(acc[2 * i + 1]));
+  *reinterpret_cast<uint4*>(out + t * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// WPT warps of a CTA share a token: 1 with tokens enough to fill the GPU, else 8.
+template <bool BF16, bool E4M3, bool DOT, int WPT>
+__global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
+    const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ y, int64_t tokens, int64_t S, int cols, int nblocks,
+    const int32_t* __restrict__ rows, int k, const float* __restrict__ weights, __nv_bfloat16* __restrict__ out,
+    uint8_t* __restrict__ codes, float* __restrict__ scale, float* __restrict__ grad_weights) {
+  constexpr int kWarps = kThreadsT / 32, kTokens = kWarps / WPT, G = kTogether;
+  __shared__ float part[WPT > 1 ? kWarps : 1][G];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + warp / WPT;
+  if (WPT == 1 && t >= tokens) return;      // WPT > 1: the grid is the tokens
+  const Slots s(rows, weights, t, k, S, lane);
+  for (int j0 = 0; j0 < k; j0 += G) {
+    int64_t r[G];
+    float w[G], dot[G];
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      r[u] = __shfl_sync(kFull, s.row, j0 + u);
+      w[u] = __shfl_sync(kFull, s.weight, j0 + u);
+      dot[u] = 0.f;
+    }
+    for (uint32_t piece = static_cast<uint32_t>(warp % WPT) * 256; piece < static_cast<uint32_t>(cols); piece += WPT * 256) {
+      const uint32_t c = piece + lane * 8;
+      const bool in = c < static_cast<uint32_t>(cols);
+      Eight<__nv_bfloat16> a, b[G];
+      if (in) a.load(g + t * cols + c);
+      else a.zero();
+      if (DOT) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          if (r[u] >= 0 && in) b[u].load(y + r[u] * cols + c);
+          else b[u].zero();
+        }
+      }
+      uint2 code = make_uint2(0, 0);
+      float sc = 0.f;
+      if (E4M3) {
+        const float m = block_amax16(a);
+        code = encode(a, __fdiv_rn(448.f, m));
+        sc = __fdiv_rn(m, 448.f);
+      }
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        if (r[u] < 0) continue;
+        if (DOT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 p = a.pair(i), q = b[u].pair(i);
+            dot[u] = fmaf(p.x, q.x, fmaf(p.y, q.y, dot[u]));
+          }
+        }
+        if (!in) continue;
+        if (BF16) *reinterpret_cast<uint4*>(out + r[u] * cols + c) = weights ? scaled(a.v, w[u]) : a.v;
+        if (E4M3) {
+          *reinterpret_cast<uint2*>(codes + r[u] * cols + c) = code;
+          if ((lane & 15) == 0) scale[r[u] * nblocks + (c >> 7)] = sc * w[u];
+        }
+      }
+    }
+    if (DOT) {
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) dot[u] += __shfl_xor_sync(kFull, dot[u], d);
+      }
+      if (WPT > 1) {
+        if (lane == 0) {
+#pragma unroll
+          for (int u = 0; u < G; ++u) part[warp][u] = dot[u];
+        }
+        __syncthreads();
+        if (warp == 0 && lane < G && j0 + lane < k) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < WPT; ++i) sum += part[i][lane];
+          grad_weights[t * k + j0 + lane] = sum;
+        }
+        __syncthreads();
+      } else if (lane == 0) {
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+          if (j0 + u < k) grad_weights[t * k + j0 + u] = dot[u];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_sort_experts(const SortArgs& a, const char** msg) {
+  int ctas = 1;
+  while (ctas < 8 && a.n > 8192ll * ctas) ctas *= 2;
+  // a warp's run, in whole warps of slots
+  const int64_t run = ((a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  const size_t smem = static_cast<size_t>(kSortWarps + 2) * a.E * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) {
+      *msg = cudaGetErrorString(e);
+      return static_cast<int>(e);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_experts_kernel, a.ids, a.n, a.E, run, ctas, a.offsets, a.rows, a.slots);
+  if (e != cudaSuccess) {
+    *msg = cudaGetErrorString(e);
+    return static_cast<int>(e);
+  }
+  return 0;
+}
+
+int launch_dispatch(const TokenArgs& a, const char** msg) {
+  const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
+  const int segs = static_cast<int>((a.cols + 256 * kPieces - 1) / (256 * kPieces));
+  const int64_t grid = (a.T * segs + kThreadsT / 32 - 1) / (kThreadsT / 32);
+  if (grid > INT32_MAX) {
+    *msg = "too many blocks";
+    return -1;
+  }
+  const auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
+        static_cast<const __nv_bfloat16*>(a.x), a.T, a.S, cols, segs, nb, a.rows, a.k, a.weights,
+        static_cast<__nv_bfloat16*>(a.out), static_cast<uint8_t*>(a.codes), a.scale);
+  };
+  if (a.out && a.codes) go(dispatch_kernel<true, true>);
+  else if (a.out) go(dispatch_kernel<true, false>);
+  else go(dispatch_kernel<false, true>);
+  return last_error(msg);
+}
+
+int launch_combine(const TokenArgs& a, const char** msg) {
+  const int segs = static_cast<int>((a.cols + 255) / 256);
+  const int64_t grid = (a.T * segs + kThreadsT / 32 - 1) / (kThreadsT / 32);
+  if (grid > INT32_MAX) {
+    *msg = "too many blocks";
+    return -1;
+  }
+  combine_kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
+      static_cast<const __nv_bfloat16*>(a.y), a.T, a.S, static_cast<int>(a.cols), segs, a.rows, a.k, a.weights,
+      static_cast<__nv_bfloat16*>(a.out));
+  return last_error(msg);
+}
+
+int launch_combine_backward(const TokenArgs& a, const char** msg) {
+  const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
+  const bool share = a.T < 16ll * a.num_sms;
+  const int64_t grid = share ? a.T : (a.T + kThreadsT / 32 - 1) / (kThreadsT / 32);
+  const auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
+        static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.y), a.T, a.S, cols, nb, a.rows, a.k,
+        a.weights, static_cast<__nv_bfloat16*>(a.out), static_cast<uint8_t*>(a.codes), a.scale, a.grad_weights);
+  };
+  const int what = (a.out ? 4 : 0) | (a.codes ? 2 : 0) | (a.grad_weights ? 1 : 0);
+  const auto pick = [&](auto wpt) {
+    constexpr int W = decltype(wpt)::value;
+    switch (what) {
+      case 1: go(combine_backward_kernel<false, false, true, W>); break;
+      case 2: go(combine_backward_kernel<false, true, false, W>); break;
+      case 3: go(combine_backward_kernel<false, true, true, W>); break;
+      case 4: go(combine_backward_kernel<true, false, false, W>); break;
+      case 5: go(combine_backward_kernel<true, false, true, W>); break;
+      case 6: go(combine_backward_kernel<true, true, false, W>); break;
+      case 7: go(combine_backward_kernel<true, true, true, W>); break;
+    }
+  };
+  if (share) pick(std::integral_constant<int, 8>{});
+  else pick(std::integral_constant<int, 1>{});
+  return last_error(msg);
+}
+
+}  // namespace bsq

@@ -358,6 +358,105 @@ bsq_status bsq_adamw(const bsq_adamw_tensor* tensors, int32_t count, int32_t gra
                      int64_t step, double lr, double beta1, double beta2, double eps, const float* grad_scale,
                      uint32_t seed, void* stream);
 
+/* Gates of bsq_route. */
+typedef enum {
+  BSQ_GATE_SOFTMAX = 0,
+  BSQ_GATE_SIGMOID = 1
+} bsq_gate;
+
+/*
+ * bsq_route -- the router of a mixture layer: every token's k experts of the highest score and
+ * their weights.
+ *   score    without a bias the logit; with one logit + bias (softmax) or sigmoid(logit) + bias
+ *            (sigmoid), in float32.  The bias takes part in the choice alone.
+ *   ids      int32[T][k], by falling score, ties to the lowest index
+ *   weights  f32[T][k]: factor * softmax(logits)[id], or factor * sigmoid(logit[id]);
+ *            renormalize != 0: factor times the softmax over the chosen logits alone, or the
+ *            sigmoids divided by their sum over the chosen (zeros if that sum is zero)
+ * An expert whose score is a NaN or minus infinity is not chosen; slots that are left over (a
+ * token whose logits are all masked) get id -1 and weight 0.  A NaN among a token's logits
+ * makes its weights NaN.
+ * logits: dtype (bsq_dtype) [T][E]; bias: f32[E] or NULL.  1 <= k <= 32, k <= E <= 1024.
+ */
+bsq_status bsq_route(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate, int32_t renormalize,
+                     const float* bias, float factor, int32_t* ids, float* weights, void* stream);
+
+/*
+ * bsq_route_backward -- grad_logits[T][E] (dtype, fully written) from grad_weights f32[T][k]:
+ *   softmax  p_e (g_e - sum_chosen g p), g = factor * grad_weights at the chosen, else 0
+ *            (renormalize: over the chosen alone, zero elsewhere)
+ *   sigmoid  g s (1 - s), renormalize: (g - sum g s / sum s) s (1 - s) / sum s; zero elsewhere
+ * ids: bsq_route's, or any: ids outside 0..E-1 give nothing, an id given twice counts twice.
+ * The choice itself has no gradient, and so neither has the bias.
+ */
+bsq_status bsq_route_backward(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate,
+                              int32_t renormalize, float factor, const int32_t* ids, const float* grad_weights,
+                              void* grad_logits, void* stream);
+
+/*
+ * bsq_sort_experts -- places of a batch's slots when they are sorted by expert (stable: in the
+ * order of their index t * k + j within an expert).
+ * ids: int32[T][k] (bsq_route); an id outside 0..E-1 belongs to no expert.
+ * offsets: int32[E], cumulative ends, as the grouped products take them; rows: int32[T][k], each
+ * slot's row, -1 for a slot of no expert; slots: int32[T * k] or NULL, each row's slot, -1
+ * for rows from offsets[E-1] on.  1 <= k <= 32, E <= 1024, T * k < 2^31.
+ */
+bsq_status bsq_sort_experts(const int32_t* ids, int64_t T, int32_t k, int64_t E, int32_t* offsets, int32_t* rows,
+                            int32_t* slots, void* stream);
+
+/*
+ * bsq_dispatch -- tokens to their experts' rows, out[rows[t][j]] = weights[t][j] * x[t], as BF16
+ * rows (out bf16[S][K], rounded once), as the operand of the bsq_fp8_* products (codes u8[S][K]
+ * and scale f32[S][ceil(K/128)]: bsq_quantize_e4m3's codes and scales of x[t] in 1 x 128
+ * blocks, the scale times the weight), or both from one reading of x.
+ * x: bf16[T][K], K % 8 == 0 (with codes K % 16); rows: int32[T][k], distinct (bsq_sort_experts);
+ * rows outside 0..S-1 are left out.  weights: f32[T][k] or NULL for 1.  Rows that no slot owns
+ * are not written.  out or codes may be NULL; codes and scale come together.  1 <= k <= 32.
+ * The gradient of x is bsq_combine of the rows' gradient with the same rows and weights, that of
+ * the weights bsq_combine_backward's grad_weights with x in the place of grad_out.
+ */
+bsq_status bsq_dispatch(const void* x, int64_t T, int64_t K, const int32_t* rows, int32_t k, const float* weights, int64_t S,
+                        void* out, void* codes, float* scale, void* stream);
+
+/*
+ * bsq_combine -- rows back to their tokens, out[t] = sum_j weights[t][j] * y[rows[t][j]], in the
+ * order of j in float32, rounded once.  y: bf16[S][N]; out: bf16[T][N], fully written (a token
+ * without rows gets zeros); N % 8 == 0; rows, weights and k as for bsq_dispatch, but rows need
+ * not be distinct.  Rows that no slot names are not read.
+ */
+bsq_status bsq_combine(const void* y, int64_t S, int64_t N, const int32_t* rows, int32_t k, const float* weights, int64_t T,
+                       void* out, void* stream);
+
+/*
+ * bsq_combine_backward -- the gradients of bsq_combine from grad_out bf16[T][N]:
+ *   grad_y[rows[t][j]] = weights[t][j] * grad_out[t], in the types that bsq_dispatch writes (BF16 for
+ *   the weight gradient, codes and scale for bsq_fp8_grouped_dgrad), rows distinct;
+ *   grad_weights[t][j] = grad_out[t] . y[rows[t][j]] in float32, 0 for a slot without a row.
+ * grad_y, codes with scale, and grad_weights may each be NULL; y is read for grad_weights alone.
+ */
+bsq_status bsq_combine_backward(const void* grad_out, const void* y, int64_t S, int64_t N, const int32_t* rows, int32_t k,
+                                const float* weights, int64_t T, void* grad_y, void* codes, float* scale, float* grad_weights,
+                                void* stream);
+
+/*
+ * bsq_fp4_forward -- y[M][N] = X[M][K] deq(W)[N][K]^T of a BF16 X and a 4-bit W (BSQ_MXFP4 or
+ * BSQ_NVFP4, K % 32 == 0, N % 8 == 0), dequantized by the rule above, accumulated in FP32 and
+ * rounded once: for decoding.  Up to 64 rows stream W through a kernel of their own; more take
+ * bsq_linear_forward's.  y: bf16[M][N], fully written; K == 0 gives zeros.  K <= 2^24.
+ */
+bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* w_data, const void* w_scale,
+                           const float* w_tensor_scale, int64_t N, int64_t K, void* y, void* stream);
+
+/*
+ * bsq_fp4_grouped_forward -- that product per expert: rows [offsets[e-1] or 0, offsets[e]) against
+ * W[e].  W: [E][N][K], w_tensor_scale f32[E]; offsets, rows past offsets[E-1] (never read or
+ * written) and the limits on E are those of bsq_grouped_dgrad.  Any S, but made for decoding: an
+ * expert's W is decoded again for every 32 of its rows.  K == 0 with S > 0 is unsupported.
+ */
+bsq_status bsq_fp4_grouped_forward(const void* x, int64_t S, int32_t w_fmt, const void* w_data, const void* w_scale,
+                                   const float* w_tensor_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
+                                   void* y, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* bsq_status_string(int32_t status);
 
