@@ -415,8 +415,8 @@ def _operand(name, t, dtypes, dims, dev):
 
 
 def _given(name, t, dtype, shape, dev):
-    """A further operand of a known shape."""
-    if not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+    """A further operand of a known shape, where there is one."""
+    if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
         _dense(t, (dtype,), name)
         raise ValueError(f"{name}: {tuple(t.shape)} on {t.device}; {tuple(shape)} on cuda:{dev} is wanted")
 
@@ -443,15 +443,22 @@ def route(logits, k, gate="softmax", renormalize=True, bias=None, factor=1.0, id
     over the chosen logits (renormalize=False: over all), or the sigmoids, divided by their sum
     (renormalize=False: as they are).  bias (float32 [E]) is added to the logit (sigmoid gate: to its sigmoid) for the
     choice alone.  A slot that no expert can fill, because logits are minus infinity or NaN, gets id -1 and weight 0."""
-    dev = _first("route", logits, _DTYPES, 2)
-    T, E = logits.shape
+    # one expression for the common case, here and below; what is wrong is looked for only when it fails
+    if not (logits is not None and logits.dtype in _DTYPES and logits.get_device() == _current_device() and logits.is_contiguous()
+            and len(logits.shape) == 2 and (bias is None or bias.dtype is torch.float32 and bias.get_device() == logits.get_device()
+                                            and bias.shape == logits.shape[1:] and bias.is_contiguous())):
+        dev = _first("route", logits, _DTYPES, 2)
+        _given("route: bias", bias, torch.float32, logits.shape[1:], dev)
     if gate not in _GATES:
         raise ValueError(f"route: gate {gate!r}; 'softmax' or 'sigmoid' is wanted")
-    if bias is not None:
-        _given("route: bias", bias, torch.float32, (E,), dev)
-    ids = _new(ids, (T, k), _I32, logits, stream, "route: ids")
-    weights = _new(weights, (T, k), torch.float32, logits, stream, "route: weights")
-    status = (_lib or lib()).bsq_route(_DTYPES[logits.dtype], logits.data_ptr(), T, E, k, _GATES[gate], bool(renormalize),
+    T, E = logits.shape
+    if stream is None and ids is None and weights is None:
+        ids = torch.empty((T, k), dtype=_I32, device=logits.device)
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    else:
+        ids = _out(ids, (T, k), _I32, logits, stream, "route: ids")
+        weights = _out(weights, (T, k), torch.float32, logits, stream, "route: weights")
+    status = (_lib or lib()).bsq_route(_DTYPES[logits.dtype], logits.data_ptr(), T, E, k, _GATES[gate], renormalize,
                                        None if bias is None else bias.data_ptr(), factor, ids.data_ptr(), weights.data_ptr(),
                                        _raw_stream(stream, logits))
     if status:
@@ -462,18 +469,21 @@ def route(logits, k, gate="softmax", renormalize=True, bias=None, factor=1.0, id
 def route_backward(logits, ids, grad_weights, gate="softmax", renormalize=True, factor=1.0, out=None, stream=None):
     """The gradient of `route`'s logits (their type) from that of its weights; gate, renormalize and factor
     as they were there."""
-    dev = _first("route_backward", logits, _DTYPES, 2)
-    T, E = logits.shape
+    if not (logits is not None and ids is not None and grad_weights is not None and logits.dtype in _DTYPES and ids.dtype is _I32
+            and grad_weights.dtype is torch.float32 and logits.get_device() == ids.get_device() == grad_weights.get_device() == _current_device()
+            and len(logits.shape) == len(ids.shape) == 2 and ids.shape[0] == logits.shape[0] and grad_weights.shape == ids.shape
+            and logits.is_contiguous() and ids.is_contiguous() and grad_weights.is_contiguous()):
+        dev = _first("route_backward", logits, _DTYPES, 2)
+        _operand("route_backward: ids", ids, (_I32,), 2, dev)
+        _given("route_backward: ids", ids, _I32, (logits.shape[0], ids.shape[1]), dev)
+        _operand("route_backward: grad_weights", grad_weights, _F32, 2, dev)
+        _given("route_backward: grad_weights", grad_weights, torch.float32, tuple(ids.shape), dev)
     if gate not in _GATES:
         raise ValueError(f"route_backward: gate {gate!r}; 'softmax' or 'sigmoid' is wanted")
-    _operand("route_backward: ids", ids, (_I32,), 2, dev)
-    k = ids.shape[1]
-    _given("route_backward: ids", ids, _I32, (T, k), dev)
-    _given("route_backward: grad_weights", grad_weights, torch.float32, (T, k), dev)
-    out = _new(out, (T, E), logits.dtype, logits, stream, "route_backward")
-    status = (_lib or lib()).bsq_route_backward(_DTYPES[logits.dtype], logits.data_ptr(), T, E, k, _GATES[gate], bool(renormalize),
-                                                factor, ids.data_ptr(), grad_weights.data_ptr(), out.data_ptr(),
-                                                _raw_stream(stream, logits))
+    T, E = logits.shape
+    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device) if out is None and stream is None else _out(out, (T, E), logits.dtype, logits, stream, "route_backward")
+    status = (_lib or lib()).bsq_route_backward(_DTYPES[logits.dtype], logits.data_ptr(), T, E, ids.shape[1], _GATES[gate], renormalize,
+                                                factor, ids.data_ptr(), grad_weights.data_ptr(), out.data_ptr(), _raw_stream(stream, logits))
     if status:
         _check(status)
     return out
@@ -483,12 +493,13 @@ def sort_experts(ids, E, want_slots=True, offsets=None, rows=None, slots=None, s
     """(offsets int32 [E], rows int32 [T, k], slots int32 [T * k] or None): where each slot's row is when the slots of
     ids [T, k] are sorted by expert (stable; -1 for an id outside 0..E-1), the cumulative ends of the experts'
     rows, and the slot of every row (-1 from the last end on)."""
-    _first("sort_experts", ids, (_I32,), 2)
+    if not (ids is not None and ids.dtype is _I32 and ids.get_device() == _current_device() and len(ids.shape) == 2 and ids.is_contiguous()):
+        _first("sort_experts", ids, (_I32,), 2)
     T, k = ids.shape
-    offsets = _new(offsets, (E,), _I32, ids, stream, "sort_experts: offsets")
-    rows = _new(rows, (T, k), _I32, ids, stream, "sort_experts: rows")
-    if want_slots or slots is not None:
-        slots = _new(slots, (T * k,), _I32, ids, stream, "sort_experts: slots")
+    offsets = torch.empty(E, dtype=_I32, device=ids.device) if offsets is None and stream is None else _out(offsets, (E,), _I32, ids, stream, "sort_experts: offsets")
+    rows = torch.empty((T, k), dtype=_I32, device=ids.device) if rows is None and stream is None else _out(rows, (T, k), _I32, ids, stream, "sort_experts: rows")
+    if slots is not None or want_slots:
+        slots = torch.empty(T * k, dtype=_I32, device=ids.device) if slots is None and stream is None else _out(slots, (T * k,), _I32, ids, stream, "sort_experts: slots")
     status = (_lib or lib()).bsq_sort_experts(ids.data_ptr(), T, k, E, offsets.data_ptr(), rows.data_ptr(),
                                               None if slots is None else slots.data_ptr(), _raw_stream(stream, ids))
     if status:
@@ -496,14 +507,36 @@ def sort_experts(ids, E, want_slots=True, offsets=None, rows=None, slots=None, s
     return offsets, rows, slots
 
 
+def _tokens(name, x, rows, weights, of_rows):
+    """x: BF16 [n, cols]; rows: int32 [T, k], with T == n unless x itself holds rows; weights: float32 [T, k] or None."""
+    if not (x is not None and rows is not None and x.dtype is _BF16 and rows.dtype is _I32 and x.get_device() == rows.get_device() == _current_device()
+            and len(x.shape) == len(rows.shape) == 2 and (of_rows or x.shape[0] == rows.shape[0]) and x.is_contiguous() and rows.is_contiguous()
+            and (weights is None or weights.dtype is torch.float32 and weights.shape == rows.shape and weights.get_device() == rows.get_device()
+                 and weights.is_contiguous())):
+        dev = _first(name, x, (_BF16,), 2)
+        _operand(f"{name}: rows", rows, (_I32,), 2, dev)
+        if not of_rows:
+            _given(f"{name}: rows", rows, _I32, (x.shape[0], rows.shape[1]), dev)
+        _given(f"{name}: weights", weights, torch.float32, tuple(rows.shape), dev)
+
+
 def _written(name, S, cols, bf16, e4m3, out, codes, scale, like, stream):
-    """The rows that dispatch and combine_backward write, and their addresses."""
+    """The rows that dispatch and combine_backward write, None for what is not wanted."""
+    if stream is None and out is None and codes is None and scale is None:
+        dev = like.device
+        return (torch.empty((S, cols), dtype=_BF16, device=dev) if bf16 else None,
+                torch.empty((S, cols), dtype=torch.uint8, device=dev) if e4m3 else None,
+                torch.empty((S, (cols + 127) // 128), dtype=torch.float32, device=dev) if e4m3 else None)
     if bf16 or out is not None:
-        out = _new(out, (S, cols), _BF16, like, stream, f"{name}: rows")
+        out = _out(out, (S, cols), _BF16, like, stream, f"{name}: rows")
     if e4m3 or codes is not None or scale is not None:
-        codes = _new(codes, (S, cols), torch.uint8, like, stream, f"{name}: codes")
-        scale = _new(scale, (S, (cols + 127) // 128), torch.float32, like, stream, f"{name}: scale")
-    return (out, codes, scale), tuple(None if t is None else t.data_ptr() for t in (out, codes, scale))
+        codes = _out(codes, (S, cols), torch.uint8, like, stream, f"{name}: codes")
+        scale = _out(scale, (S, (cols + 127) // 128), torch.float32, like, stream, f"{name}: scale")
+    return out, codes, scale
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def dispatch(x, rows, weights=None, S=None, bf16=True, e4m3=False, out=None, codes=None, scale=None, stream=None):
@@ -511,37 +544,29 @@ def dispatch(x, rows, weights=None, S=None, bf16=True, e4m3=False, out=None, cod
     [T, k], or None for 1), as BF16 rows [S, K], as E4M3 codes [S, K] with scales [S, ceil(K / 128)] (quantize_e4m3's
     of the token, the scales times the weight), or both; None for what is not wanted.  S: rows in all, as many as
     there are slots if not given.  Rows that no slot owns are not written."""
-    dev = _first("dispatch", x, (_BF16,), 2)
+    _tokens("dispatch", x, rows, weights, False)
     T, K = x.shape
-    _operand("dispatch: rows", rows, (_I32,), 2, dev)
     k = rows.shape[1]
-    _given("dispatch: rows", rows, _I32, (T, k), dev)
-    if weights is not None:
-        _given("dispatch: weights", weights, torch.float32, (T, k), dev)
     if S is None:
         S = next((t.shape[0] for t in (out, codes, scale) if t is not None), T * k)
     if not (bf16 or e4m3 or out is not None or codes is not None or scale is not None):
         raise ValueError("dispatch: neither BF16 rows nor E4M3 codes are wanted")
-    made, at = _written("dispatch", S, K, bf16, e4m3, out, codes, scale, x, stream)
-    status = (_lib or lib()).bsq_dispatch(x.data_ptr(), T, K, rows.data_ptr(), k, None if weights is None else weights.data_ptr(), S,
-                                          *at, _raw_stream(stream, x))
+    out, codes, scale = _written("dispatch", S, K, bf16, e4m3, out, codes, scale, x, stream)
+    status = (_lib or lib()).bsq_dispatch(x.data_ptr(), T, K, rows.data_ptr(), k, _at(weights), S, _at(out), _at(codes), _at(scale),
+                                          _raw_stream(stream, x))
     if status:
         _check(status)
-    return made
+    return out, codes, scale
 
 
 def combine(y, rows, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * y[rows[t, j]] (BF16 [T, N]) of the BF16 rows y [S, N]; weights float32 [T, k], or None
     for 1.  A row outside y adds nothing.  Also the gradient of dispatch's x, from that of its rows."""
-    dev = _first("combine", y, (_BF16,), 2)
+    _tokens("combine", y, rows, weights, True)
     S, N = y.shape
-    _operand("combine: rows", rows, (_I32,), 2, dev)
     T, k = rows.shape
-    if weights is not None:
-        _given("combine: weights", weights, torch.float32, (T, k), dev)
-    out = _new(out, (T, N), _BF16, y, stream, "combine")
-    status = (_lib or lib()).bsq_combine(y.data_ptr(), S, N, rows.data_ptr(), k, None if weights is None else weights.data_ptr(), T,
-                                         out.data_ptr(), _raw_stream(stream, y))
+    out = torch.empty((T, N), dtype=_BF16, device=y.device) if out is None and stream is None else _out(out, (T, N), _BF16, y, stream, "combine")
+    status = (_lib or lib()).bsq_combine(y.data_ptr(), S, N, rows.data_ptr(), k, _at(weights), T, out.data_ptr(), _raw_stream(stream, y))
     if status:
         _check(status)
     return out
@@ -552,15 +577,11 @@ def combine_backward(grad_out, y, rows, weights=None, bf16=True, e4m3=False, wan
     """(grad_y, codes, scale, grad_weights) of combine from grad_out [T, N]: weights[t, j] * grad_out[t] at each row, as BF16
     and E4M3 rows as dispatch writes them, and grad_out[t] . y[rows[t, j]] (float32 [T, k]); None for what is not wanted.
     y may be None without want_weights; then S rows are written, as many as there are slots if not given."""
-    dev = _first("combine_backward", grad_out, (_BF16,), 2)
+    _tokens("combine_backward", grad_out, rows, weights, False)
     T, N = grad_out.shape
-    _operand("combine_backward: rows", rows, (_I32,), 2, dev)
     k = rows.shape[1]
-    _given("combine_backward: rows", rows, _I32, (T, k), dev)
-    if weights is not None:
-        _given("combine_backward: weights", weights, torch.float32, (T, k), dev)
     if y is not None:
-        _operand("combine_backward: y", y, (_BF16,), 2, dev)
+        _operand("combine_backward: y", y, (_BF16,), 2, grad_out.get_device())
         if y.shape[1] != N or S not in (None, y.shape[0]):
             raise ValueError(f"combine_backward: y {tuple(y.shape)}; {'any' if S is None else S} rows of {N} are wanted")
         S = y.shape[0]
@@ -568,20 +589,20 @@ def combine_backward(grad_out, y, rows, weights=None, bf16=True, e4m3=False, wan
         raise ValueError("combine_backward: the gradient of the weights needs y")
     if S is None:
         S = next((t.shape[0] for t in (grad_y, codes, scale) if t is not None), T * k)
-    made, at = _written("combine_backward", S, N, bf16, e4m3, grad_y, codes, scale, grad_out, stream)
+    grad_y, codes, scale = _written("combine_backward", S, N, bf16, e4m3, grad_y, codes, scale, grad_out, stream)
     if want_weights or grad_weights is not None:
         grad_weights = _new(grad_weights, (T, k), torch.float32, grad_out, stream, "combine_backward: grad_weights")
-    status = (_lib or lib()).bsq_combine_backward(
-        grad_out.data_ptr(), None if y is None else y.data_ptr(), S, N, rows.data_ptr(), k,
-        None if weights is None else weights.data_ptr(), T, *at, None if grad_weights is None else grad_weights.data_ptr(),
-        _raw_stream(stream, grad_out))
+    status = (_lib or lib()).bsq_combine_backward(grad_out.data_ptr(), _at(y), S, N, rows.data_ptr(), k, _at(weights), T, _at(grad_y), _at(codes),
+                                                  _at(scale), _at(grad_weights), _raw_stream(stream, grad_out))
     if status:
         _check(status)
-    return (*made, grad_weights)
+    return grad_y, codes, scale, grad_weights
 
 
 def _fp4(name, x, w, offsets, out, stream):
-    dev = _first(name, x, (_BF16,), 2)
+    if not (x is not None and x.dtype is _BF16 and x.get_device() == _current_device() and len(x.shape) == 2 and x.is_contiguous()):
+        _first(name, x, (_BF16,), 2)
+    dev = x.get_device()
     rows, k = x.shape
     wd, ws, ts, batch, n = w.data, w.scale, w.tensor_scale, w.batch, w.rows
     group = 16 if w.fmt == BSQ_NVFP4 else 32

@@ -8,12 +8,14 @@
 //             (renormalized: the same over the chosen, all other gradients zero)
 //   sigmoid   dl_j = g_j s_j (1 - s_j), renormalized (g_j - sum g s / sum s) s_j (1 - s_j) / sum s
 //
-// A warp per token: lane l holds experts l, l + 32, ... in registers.  Scores are compared as
-// integers of the same order, so that one warp-wide integer maximum finds the best and a
-// minimum over indices breaks ties; a chosen expert's key becomes zero, the key of an expert
-// that cannot be chosen (a NaN or minus infinity).  All sums are float32.
+// A warp per token, V = E / 32 experts a lane in registers.  Scores are compared as
+// integers of the same order, so that one warp-wide integer maximum finds the best and the
+// first lane that has it the lowest index; a chosen expert's key leaves, and the key of an expert
+// that cannot be chosen (a NaN or minus infinity) is zero.  All sums are float32.  Bound by the
+// instructions of the rounds.
 #include <cuda_bf16.h>
 
+#include "bsq_lanes.cuh"
 #include "bsq_moe_internal.h"
 #include "../../include/bsq.h"
 
@@ -22,7 +24,7 @@ namespace bsq {
 namespace {
 
 constexpr int kWarpsR = 4;    // tokens a CTA
-constexpr uint32_t kFull = 0xffffffffu;
+constexpr int log2_of(int v) { return v < 2 ? 0 : 1 + log2_of(v / 2); }
 
 __device__ __forceinline__ float load(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
@@ -47,51 +49,89 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
-// V: experts a lane.
+// A lane's experts by falling score, equal ones by rising index: neighbours are exchanged in turn, and
+// only for a higher score; V rounds put V in order.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V], uint32_t (&e)[V]) {
+#pragma unroll
+  for (int n = 0; n < V; ++n) {
+#pragma unroll
+    for (int i = n & 1; i + 1 < V; i += 2) {
+      const bool swap = key[i + 1] > key[i];
+      const uint32_t k0 = swap ? key[i + 1] : key[i], e0 = swap ? e[i + 1] : e[i];
+      key[i + 1] = swap ? key[i] : key[i + 1];
+      e[i + 1] = swap ? e[i] : e[i + 1];
+      key[i] = k0;
+      e[i] = e0;
+    }
+  }
+}
+
+// A lane's V logits; minus infinity past the last.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int lane, int E, float (&l)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = lane * V + v < E ? load(row + lane * V + v) : -INFINITY;
+}
+
+// V: experts a lane.  Up to eight, a lane puts its own in order first, so that each of the k rounds
+// looks at one key a lane; with more, the order costs more than it saves.
 template <typename T, int V>
 __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int k,
                                                             int gate, bool renorm, const float* __restrict__ bias,
                                                             float factor, int32_t* __restrict__ ids,
                                                             float* __restrict__ weights) {
+  __shared__ int32_t taken[kWarpsR][32];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarpsR + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= tokens) return;
+  int32_t* mine = taken[threadIdx.x >> 5];
   const T* row = logits + t * E;
+  constexpr bool kOrdered = V <= 8;
   float l[V];
-  uint32_t key[V];
+  uint32_t key[V], expert[V];
   bool nan = false;
+  load_row(row, lane, E, l);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = 32 * v + lane;
-    l[v] = e < E ? load(row + e) : -INFINITY;
-    nan |= l[v] != l[v];
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = 32 * v + lane;
+    const int e = lane * V + v;
     float s = l[v];
+    nan |= s != s;
     if (bias && e < E) s = (gate == BSQ_GATE_SIGMOID ? sigmoid(s) : s) + __ldg(bias + e);
     key[v] = order_of(s);
+    expert[v] = e;
   }
   nan = __any_sync(kFull, nan);
-  int id = -1;             // lane j: slot j's expert and its logit
-  float chosen = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = 0, e = kFull;
-    float at = 0.f;
+  if (kOrdered) sort_keys(key, expert);
+  int j = 0;
+  for (; j < k; ++j) {
+    uint32_t best = key[0], e = expert[0];
+    if (!kOrdered) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] > best) best = key[v], e = 32 * v + lane, at = l[v];
+      for (int v = 1; v < V; ++v)
+        if (key[v] > best) best = key[v], e = expert[v];
+    }
     const uint32_t top = __reduce_max_sync(kFull, best);
     if (top == 0) break;   // the rest cannot be chosen
-    const uint32_t winner = __reduce_min_sync(kFull, best == top ? e : kFull);
-    const float logit = __shfl_sync(kFull, at, winner & 31);
-    if (lane == j) id = static_cast<int>(winner), chosen = logit;
+    // the first lane of equal ones holds the lowest index
+    const uint32_t equal = __ballot_sync(kFull, best == top);
+    if (lane == __ffs(equal) - 1) {
+      mine[j] = static_cast<int32_t>(e);
+      if (kOrdered) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (winner == 32u * v + lane) key[v] = 0;
+        for (int v = 0; v + 1 < V; ++v) key[v] = key[v + 1], expert[v] = expert[v + 1];
+        key[V - 1] = 0;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (expert[v] == e) key[v] = 0;
+      }
+    }
   }
+  __syncwarp();
+  const int id = lane < j ? mine[lane] : -1;     // lane j: slot j's expert
   const bool have = id >= 0;
+  const float chosen = have ? load(row + id) : -INFINITY;
   float w;
   if (gate == BSQ_GATE_SOFTMAX) {
     float m = chosen, sum = 0.f;
@@ -105,7 +145,7 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
       sum = ex;
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum += 32 * v + lane < E ? expf(l[v] - m) : 0.f;
+      for (int v = 0; v < V; ++v) sum += lane * V + v < E ? expf(l[v] - m) : 0.f;
     }
     w = ex / warp_sum(sum);
   } else {
@@ -121,33 +161,37 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
   }
 }
 
+// The row's gradient that all experts share (-p mean, or zero) goes to shared memory, the lanes of
+// the chosen add theirs, and the row is written once.
 template <typename T, int V>
 __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E,
                                                                      int k, int gate, bool renorm, float factor,
                                                                      const int32_t* __restrict__ ids,
                                                                      const float* __restrict__ grad_weights,
                                                                      T* __restrict__ grad_logits) {
+  __shared__ float grads[kWarpsR][32 * V];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarpsR + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= tokens) return;
   const T* row = logits + t * E;
+  float* mine = grads[threadIdx.x >> 5];
+  const bool every = gate == BSQ_GATE_SOFTMAX && !renorm;   // every expert's gradient, not the chosen ones' alone
+  float p[V];
+  if (every) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = 32 * v + lane < E ? load(row + 32 * v + lane) : -INFINITY;
+  }
   const int id = lane < k ? __ldg(ids + t * k + lane) : -1;
   const bool have = static_cast<unsigned>(id) < static_cast<unsigned>(E);
   const float g = have ? factor * __ldg(grad_weights + t * k + lane) : 0.f;
   const float chosen = have ? load(row + id) : -INFINITY;
-  const bool any = __any_sync(kFull, have);
-  const bool full = gate == BSQ_GATE_SOFTMAX && !renorm && any;   // every expert's gradient, not the chosen ones' alone
-  float p[V], mean = 0.f, d = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) p[v] = 0.f;
+  const bool full = every && __any_sync(kFull, have);
+  float mean = 0.f, d = 0.f;
   if (gate == BSQ_GATE_SOFTMAX) {
     float m = chosen, sum = 0.f;
     if (full) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        p[v] = 32 * v + lane < E ? load(row + 32 * v + lane) : -INFINITY;
-        m = fmaxf(m, p[v]);
-      }
+      for (int v = 0; v < V; ++v) m = fmaxf(m, p[v]);
     }
     m = warp_max(m);
     const float ex = have ? expf(chosen - m) : 0.f;
@@ -164,10 +208,8 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
     const float q = have ? ex / sum : 0.f;
     mean = warp_sum(g * q);
     d = full ? g * q : q * (g - mean);
-    if (full) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) p[v] = -(p[v] / sum) * mean;
-    }
+    for (int v = 0; v < V; ++v) p[v] = full ? -(p[v] / sum) * mean : 0.f;
   } else {
     const float s = have ? sigmoid(chosen) : 0.f;
     d = g * s * (1.f - s);
@@ -175,18 +217,23 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
       const float sum = warp_sum(s), mass = warp_sum(g * s);
       d = sum != 0.f ? (g - mass / sum) / sum * s * (1.f - s) : 0.f;
     }
-  }
-  if (!have) d = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = __shfl_sync(kFull, id, j);
-    const float add = __shfl_sync(kFull, d, j);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == 32 * v + lane) p[v] += add;
+    for (int v = 0; v < V; ++v) p[v] = 0.f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine[32 * v + lane] = p[v];
+  __syncwarp();
+  // one lane an expert adds; ids that are given twice take turns, the first lane first
+  const uint32_t same = same_lanes(have ? id : 32 * V, 6 + log2_of(V));
+  const int before = __popc(same & ((1u << lane) - 1u));
+  const int turns = __reduce_max_sync(kFull, have ? before : 0);
+  for (int n = 0; n <= turns; ++n) {
+    if (have && before == n) mine[id] += d;
+    __syncwarp();
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (32 * v + lane < E) store(grad_logits + t * E + 32 * v + lane, p[v]);
+    if (32 * v + lane < E) store(grad_logits + t * E + 32 * v + lane, mine[32 * v + lane]);
 }
 
 template <typename T, int V>

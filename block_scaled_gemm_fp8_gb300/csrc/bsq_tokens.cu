@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 
 #include "bsq_e4m3.cuh"
+#include "bsq_lanes.cuh"
 #include "bsq_moe_internal.h"
 #include "bsq_ptx.cuh"
 #include "../../include/bsq.h"
@@ -18,8 +19,6 @@
 namespace bsq {
 
 namespace {
-
-constexpr uint32_t kFull = 0xffffffffu;
 
 int last_error(const char** msg) {
   const cudaError_t e = cudaGetLastError();
@@ -30,12 +29,27 @@ int last_error(const char** msg) {
 
 // ---------------------------------------------------------------- sort
 constexpr int kSortWarps = 32;
-constexpr int kAheadS = 4;       // ids a lane loads before the first is counted
+constexpr int kAheadS = 4;       // ids a lane loads before the first is counted, where it does not hold them all
+
+// Counts a warp's 32 slots: the number of slots of the same expert before each, within the warp's run;
+// `mine`: the warp's counters.  Lanes of one expert find one another by votes, so nothing is added
+// atomically.  bits: of E.
+__device__ __forceinline__ int32_t count_slots(int32_t* mine, int e, bool in, uint32_t below, int E, int bits) {
+  const uint32_t same = same_lanes(in ? e : E, bits);
+  const int32_t before = in ? mine[e] + __popc(same & below) : 0;
+  __syncwarp();
+  if (in && (same & below) == 0) mine[e] += __popc(same);
+  __syncwarp();
+  return before;
+}
 
 // A counting sort in one launch of one cluster.  Every warp counts its run of slots in
-// counters of its own (lanes of one expert find one another by match, so nothing is
-// added atomically), the counts become first places (over warps, CTAs through
-// distributed shared memory, then experts), and every warp goes over its run again.
+// counters of its own, the counts become first places (over warps, CTAs through distributed
+// shared memory, then experts), and every slot's place is its expert's first plus its rank.
+// HELD: slots a lane holds in registers, 32 HELD a warp's run; 0: any run, read and counted twice.
+// Bound by latency: 16384 slots on 64 experts take 4.7 us, of which a launch and two barriers of
+// the cluster are 3.
+template <int HELD>
 __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
                                                                       int64_t run, int ctas, int32_t* __restrict__ offsets,
                                                                       int32_t* __restrict__ rows, int32_t* __restrict__ slots) {
@@ -46,32 +60,42 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
   __shared__ int32_t kept;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x);
+  const int64_t begin = min(n, (static_cast<int64_t>(rank) * kSortWarps + warp) * run), end = min(n, begin + run);
+  const uint32_t below = (1u << lane) - 1u;
+  int held[HELD > 0 ? HELD : 1], rank_of[HELD > 0 ? HELD : 1];
+#pragma unroll
+  for (int u = 0; u < HELD; ++u) held[u] = begin + 32 * u + lane < end ? __ldg(ids + begin + 32 * u + lane) : -1;
   for (int i = tid; i < kSortWarps * E; i += kSortWarps * 32) counts[i] = 0;
   __syncthreads();
   int32_t* mine = counts + warp * E;
-  const int64_t begin = min(n, (static_cast<int64_t>(rank) * kSortWarps + warp) * run), end = min(n, begin + run);
-  const uint32_t below = (1u << lane) - 1u;
+  const int bits = 32 - __clz(E);
+  const auto known = [&](int e) { return static_cast<unsigned>(e) < static_cast<unsigned>(E); };
 
-  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
-    int e[kAheadS];
+  if (HELD > 0) {
 #pragma unroll
-    for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
+    for (int u = 0; u < HELD; ++u) rank_of[u] = count_slots(mine, held[u], known(held[u]), below, E, bits);
+  } else {
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
+      int e[kAheadS];
 #pragma unroll
-    for (int u = 0; u < kAheadS; ++u) {
-      const bool in = static_cast<unsigned>(e[u]) < static_cast<unsigned>(E);
-      const uint32_t same = __match_any_sync(kFull, in ? e[u] : -1);
-      if (in && (same & below) == 0) mine[e[u]] += __popc(same);
-      __syncwarp();
+      for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+      for (int u = 0; u < kAheadS; ++u) count_slots(mine, e[u], known(e[u]), below, E, bits);
     }
   }
   __syncthreads();
   int32_t sum = 0;                          // thread e: slots of expert e in this CTA
   if (tid < E) {
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int32_t c = counts[w * E + tid];
-      counts[w * E + tid] = sum;
-      sum += c;
+#pragma unroll
+    for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+      int32_t c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * E + tid];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        counts[(w0 + w) * E + tid] = sum;
+        sum += c[w];
+      }
     }
     total[tid] = sum;
   }
@@ -80,6 +104,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
     cluster_sync();
     if (tid < E) {
       all = 0;
+#pragma unroll 8
       for (int c = 0; c < ctas; ++c) {
         const int32_t v = static_cast<int32_t>(ld_shared_cluster_u32(map_to_rank(smem_u32(total + tid), c)));
         before += c < rank ? v : 0;
@@ -96,10 +121,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
   }
   if (lane == 31) wsum[warp] = upto;
   __syncthreads();
-  int32_t ahead = lane < warp ? wsum[lane] : 0;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) ahead += __shfl_xor_sync(kFull, ahead, d);
-  upto += ahead;
+  upto += __reduce_add_sync(kFull, lane < warp ? wsum[lane] : 0);
   if (tid < E) {
     base[tid] = upto - own + before;
     if (rank == 0) offsets[tid] = upto;
@@ -109,27 +131,26 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
   if (ctas > 1) cluster_sync();
   else __syncthreads();
 
+  const auto place = [&](int64_t i, int e, int32_t at) {
+    const int32_t row = known(e) ? base[e] + at : -1;
+    if (i < end) rows[i] = row;
+    if (known(e) && slots) slots[row] = static_cast<int32_t>(i);
+  };
+  if (HELD > 0) {
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) place(begin + 32 * u + lane, held[u], rank_of[u] + (known(held[u]) ? mine[held[u]] : 0));
+  } else {
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
+      int e[kAheadS];
+#pragma unroll
+      for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+      for (int u = 0; u < kAheadS; ++u) place(i0 + 32 * u + lane, e[u], count_slots(mine, e[u], known(e[u]), below, E, bits));
+    }
+  }
   if (slots)
     for (int64_t i = static_cast<int64_t>(kept) + rank * (kSortWarps * 32) + tid; i < n; i += static_cast<int64_t>(ctas) * (kSortWarps * 32))
       slots[i] = -1;
-  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAheadS) {
-    int e[kAheadS];
-#pragma unroll
-    for (int u = 0; u < kAheadS; ++u) e[u] = i0 + 32 * u + lane < end ? __ldg(ids + i0 + 32 * u + lane) : -1;
-#pragma unroll
-    for (int u = 0; u < kAheadS; ++u) {
-      const bool in = static_cast<unsigned>(e[u]) < static_cast<unsigned>(E);
-      const uint32_t same = __match_any_sync(kFull, in ? e[u] : -1);
-      const int64_t i = i0 + 32 * u + lane;
-      int32_t place = -1;
-      if (in) place = base[e[u]] + mine[e[u]] + __popc(same & below);
-      __syncwarp();
-      if (in && (same & below) == 0) mine[e[u]] += __popc(same);
-      __syncwarp();
-      if (i < end) rows[i] = place;
-      if (in && slots) slots[place] = static_cast<int32_t>(i);
-    }
-  }
 }
 
 // ---------------------------------------------------------------- rows of a token
@@ -248,18 +269,20 @@ __global__ void __launch_bounds__(kThreadsT) combine_kernel(const __nv_bfloat16*
   *reinterpret_cast<uint4*>(out + t * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// WPT warps of a CTA share a token: 1 with tokens enough to fill the GPU, else 8.
+// WPT warps of a CTA share a token: 1 with tokens enough to fill the GPU, up to 8.
 template <bool BF16, bool E4M3, bool DOT, int WPT>
 __global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
     const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ y, int64_t tokens, int64_t S, int cols, int nblocks,
     const int32_t* __restrict__ rows, int k, const float* __restrict__ weights, __nv_bfloat16* __restrict__ out,
     uint8_t* __restrict__ codes, float* __restrict__ scale, float* __restrict__ grad_weights) {
   constexpr int kWarps = kThreadsT / 32, kTokens = kWarps / WPT, G = kTogether;
-  __shared__ float part[WPT > 1 ? kWarps : 1][G];
+  __shared__ float part[kWarps][G];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + warp / WPT;
-  if (WPT == 1 && t >= tokens) return;      // WPT > 1: the grid is the tokens
-  const Slots s(rows, weights, t, k, S, lane);
+  const int64_t own = static_cast<int64_t>(blockIdx.x) * kTokens + warp / WPT;
+  const bool there = own < tokens;          // all warps of a CTA stay together for the barriers
+  const int64_t t = there ? own : tokens - 1;
+  Slots s(rows, weights, t, k, S, lane);
+  if (!there) s.row = -1;
   for (int j0 = 0; j0 < k; j0 += G) {
     int64_t r[G];
     float w[G], dot[G];
@@ -319,14 +342,14 @@ __global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
           for (int u = 0; u < G; ++u) part[warp][u] = dot[u];
         }
         __syncthreads();
-        if (warp == 0 && lane < G && j0 + lane < k) {
+        if (there && warp % WPT == 0 && lane < G && j0 + lane < k) {
           float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < WPT; ++i) sum += part[i][lane];
+          for (int i = 0; i < WPT; ++i) sum += part[warp + i][lane];
           grad_weights[t * k + j0 + lane] = sum;
         }
         __syncthreads();
-      } else if (lane == 0) {
+      } else if (there && lane == 0) {
 #pragma unroll
         for (int u = 0; u < G; ++u)
           if (j0 + u < k) grad_weights[t * k + j0 + u] = dot[u];
@@ -338,30 +361,32 @@ __global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
 }  // namespace
 
 int launch_sort_experts(const SortArgs& a, const char** msg) {
-  int ctas = 1;
-  while (ctas < 8 && a.n > 8192ll * ctas) ctas *= 2;
+  // One CTA while a warp of it has few slots; then eight, up to which a cluster runs anywhere.
+  const int ctas = a.n <= 1024 ? 1 : 8;
   // a warp's run, in whole warps of slots
-  const int64_t run = ((a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  int64_t run = ((a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  auto kernel = sort_experts_kernel<0>;
+  if (run <= 32) kernel = sort_experts_kernel<1>;
+  else if (run <= 64) kernel = sort_experts_kernel<2>;
+  else if (run <= 128) kernel = sort_experts_kernel<4>;
+  else if (run <= 256) kernel = sort_experts_kernel<8>;
   const size_t smem = static_cast<size_t>(kSortWarps + 2) * a.E * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) {
-      *msg = cudaGetErrorString(e);
-      return static_cast<int>(e);
-    }
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, a.ids, a.n, a.E, run, ctas, a.offsets, a.rows, a.slots);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_experts_kernel, a.ids, a.n, a.E, run, ctas, a.offsets, a.rows, a.slots);
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);
     return static_cast<int>(e);
@@ -403,8 +428,8 @@ int launch_combine(const TokenArgs& a, const char** msg) {
 
 int launch_combine_backward(const TokenArgs& a, const char** msg) {
   const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
-  const bool share = a.T < 16ll * a.num_sms;
-  const int64_t grid = share ? a.T : (a.T + kThreadsT / 32 - 1) / (kThreadsT / 32);
+  const int wpt = a.T >= 64ll * a.num_sms ? 1 : a.T >= 32ll * a.num_sms ? 2 : a.T >= 16ll * a.num_sms ? 4 : 8;
+  const int64_t grid = (a.T * wpt + kThreadsT / 32 - 1) / (kThreadsT / 32);
   const auto go = [&](auto kernel) {
     kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
         static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.y), a.T, a.S, cols, nb, a.rows, a.k,
@@ -423,7 +448,9 @@ int launch_combine_backward(const TokenArgs& a, const char** msg) {
       case 7: go(combine_backward_kernel<true, true, true, W>); break;
     }
   };
-  if (share) pick(std::integral_constant<int, 8>{});
+  if (wpt == 8) pick(std::integral_constant<int, 8>{});
+  else if (wpt == 4) pick(std::integral_constant<int, 4>{});
+  else if (wpt == 2) pick(std::integral_constant<int, 2>{});
   else pick(std::integral_constant<int, 1>{});
   return last_error(msg);
 }
