@@ -48,6 +48,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// e^x for the softmax's x <= 0, as 2^(x log2 e): the rounded product adds |x| 2^-24 to the relative
+// error, as the rounding of x itself does.  expf's own splitting of x costs three times as much.
+__device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
 
 // A lane's experts by falling score, equal ones by rising index: neighbours are exchanged in turn, and
 // only for a higher score; V rounds put V in order.
@@ -76,9 +79,9 @@ __device__ __forceinline__ void load_row(const T* row, int lane, int E, float (&
 
 // V: experts a lane.  Up to eight, a lane puts its own in order first, so that each of the k rounds
 // looks at one key a lane; with more, the order costs more than it saves.
-template <typename T, int V>
+template <typename T, int V, bool SOFTMAX, bool BIAS>
 __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int k,
-                                                            int gate, bool renorm, const float* __restrict__ bias,
+                                                            bool renorm, const float* __restrict__ bias,
                                                             float factor, int32_t* __restrict__ ids,
                                                             float* __restrict__ weights) {
   __shared__ int32_t taken[kWarpsR][32];
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
     const int e = lane * V + v;
     float s = l[v];
     nan |= s != s;
-    if (bias && e < E) s = (gate == BSQ_GATE_SIGMOID ? sigmoid(s) : s) + __ldg(bias + e);
+    if (BIAS && e < E) s = (SOFTMAX ? s : sigmoid(s)) + __ldg(bias + e);
     key[v] = order_of(s);
     expert[v] = e;
   }
@@ -133,21 +136,21 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
   const bool have = id >= 0;
   const float chosen = have ? load(row + id) : -INFINITY;
   float w;
-  if (gate == BSQ_GATE_SOFTMAX) {
+  if (SOFTMAX) {
     float m = chosen, sum = 0.f;
     if (!renorm) {
 #pragma unroll
       for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
     }
     m = warp_max(m);
-    const float ex = have ? expf(chosen - m) : 0.f;
+    const float ex = have ? exp_of(chosen - m) : 0.f;
     if (renorm) {
       sum = ex;
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum += lane * V + v < E ? expf(l[v] - m) : 0.f;
+      for (int v = 0; v < V; ++v) sum += lane * V + v < E ? exp_of(l[v] - m) : 0.f;
     }
-    w = ex / warp_sum(sum);
+    w = __fdividef(ex, warp_sum(sum));     // the sum is between 1 and E
   } else {
     w = have ? sigmoid(chosen) : 0.f;
     if (renorm) {
@@ -163,9 +166,9 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
 
 // The row's gradient that all experts share (-p mean, or zero) goes to shared memory, the lanes of
 // the chosen add theirs, and the row is written once.
-template <typename T, int V>
+template <typename T, int V, bool SOFTMAX>
 __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E,
-                                                                     int k, int gate, bool renorm, float factor,
+                                                                     int k, bool renorm, float factor,
                                                                      const int32_t* __restrict__ ids,
                                                                      const float* __restrict__ grad_weights,
                                                                      T* __restrict__ grad_logits) {
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
   if (t >= tokens) return;
   const T* row = logits + t * E;
   float* mine = grads[threadIdx.x >> 5];
-  const bool every = gate == BSQ_GATE_SOFTMAX && !renorm;   // every expert's gradient, not the chosen ones' alone
+  const bool every = SOFTMAX && !renorm;   // every expert's gradient, not the chosen ones' alone
   float p[V];
   if (every) {
 #pragma unroll
@@ -187,29 +190,30 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
   const float chosen = have ? load(row + id) : -INFINITY;
   const bool full = every && __any_sync(kFull, have);
   float mean = 0.f, d = 0.f;
-  if (gate == BSQ_GATE_SOFTMAX) {
+  if (SOFTMAX) {
     float m = chosen, sum = 0.f;
     if (full) {
 #pragma unroll
       for (int v = 0; v < V; ++v) m = fmaxf(m, p[v]);
     }
     m = warp_max(m);
-    const float ex = have ? expf(chosen - m) : 0.f;
+    const float ex = have ? exp_of(chosen - m) : 0.f;
     if (full) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        p[v] = 32 * v + lane < E ? expf(p[v] - m) : 0.f;
+        p[v] = 32 * v + lane < E ? exp_of(p[v] - m) : 0.f;
         sum += p[v];
       }
     } else {
       sum = ex;
     }
     sum = warp_sum(sum);
-    const float q = have ? ex / sum : 0.f;
+    const float q = have ? __fdividef(ex, sum) : 0.f;     // the sum is between 1 and E
     mean = warp_sum(g * q);
     d = full ? g * q : q * (g - mean);
+    const float share = full ? __fdividef(-mean, sum) : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = full ? -(p[v] / sum) * mean : 0.f;
+    for (int v = 0; v < V; ++v) p[v] = full ? p[v] * share : 0.f;
   } else {
     const float s = have ? sigmoid(chosen) : 0.f;
     d = g * s * (1.f - s);
@@ -239,12 +243,20 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
 template <typename T, int V>
 void launch_v(const RouteArgs& a, unsigned grid) {
   const T* logits = static_cast<const T*>(a.logits);
-  if (a.grad_logits)
-    route_backward_kernel<T, V><<<grid, kWarpsR * 32, 0, a.stream>>>(logits, a.T, a.E, a.k, a.gate, a.renormalize, a.factor,
-                                                                     a.ids, a.grad_weights, static_cast<T*>(a.grad_logits));
-  else
-    route_kernel<T, V><<<grid, kWarpsR * 32, 0, a.stream>>>(logits, a.T, a.E, a.k, a.gate, a.renormalize, a.bias, a.factor,
-                                                            a.ids, a.weights);
+  const bool softmax = a.gate == BSQ_GATE_SOFTMAX;
+  const auto backward = [&](auto kernel) {
+    kernel<<<grid, kWarpsR * 32, 0, a.stream>>>(logits, a.T, a.E, a.k, a.renormalize, a.factor, a.ids, a.grad_weights,
+                                                static_cast<T*>(a.grad_logits));
+  };
+  const auto forward = [&](auto kernel) {
+    kernel<<<grid, kWarpsR * 32, 0, a.stream>>>(logits, a.T, a.E, a.k, a.renormalize, a.bias, a.factor, a.ids, a.weights);
+  };
+  if (a.grad_logits && softmax) backward(route_backward_kernel<T, V, true>);
+  else if (a.grad_logits) backward(route_backward_kernel<T, V, false>);
+  else if (softmax && a.bias) forward(route_kernel<T, V, true, true>);
+  else if (softmax) forward(route_kernel<T, V, true, false>);
+  else if (a.bias) forward(route_kernel<T, V, false, true>);
+  else forward(route_kernel<T, V, false, false>);
 }
 
 template <typename T>
