@@ -1,21 +1,27 @@
 // bsq_fp4_smallm.cu -- products of a few BF16 token rows with 4-bit weights (decode), dense and
 // per expert:  y[m, n] = sum_k x[m, k] deq(W)[n, k],  deq = RNE_bf16(code * RNE_bf16(scale)).
 //
-// Bound by the instructions that decode W (about 100 for 1024 codes of a warp, where the codes and
-// their scales are half a byte each), and for few columns by latency.  A CTA owns 16 MT columns of
-// y (rows of W) and the whole contraction; its warps take steps of 128 k in turn, each with a
-// ring of its own in shared memory that asynchronous copies fill some steps ahead.  A thread copies
-// 16 bytes (32 codes) of a row and reads them back as register fragments of mma.m16n8k16: the
-// order of k inside a step is free as long as both operands share it, so the 8-code words decode
-// to the pairs (c0, c4), (c1, c5), ... without a permutation (bsq_decode.cuh), and the tokens'
-// values are brought to that order instead, once for all rows of W.  CTAs begin at different
-// steps: when all asked for the same tokens' values at once, the cache line's slice held them up
-// (14336 x 5120, 8 rows: 24 us against 19).  The warps' accumulators are added in warp order
-// through shared memory, so results do not depend on timing.
+// Bound by the instructions that decode W: about 93 for 1024 codes of a warp, 36 of them masks on
+// a pipe that takes one every other cycle.  A CTA owns some rows of W (columns of y) and the
+// whole contraction; RW warps beside one another in N and KW in k, whose groups take steps of
+// 256 k in turn, each with a ring of steps in shared memory that asynchronous copies fill.  256 k
+// are 128 bytes of a row: copies of whole cache lines, for which the load unit pays by the line
+// (steps of 128 k and four bytes of scales a row and step took 4 us to ask for what a CTA holds;
+// the scales come once for the whole tile now, as they lie in memory).
+// The fragments of mma.m16n8k16 come from those rows without a permutation: the order of k inside
+// a step is free as long as both operands share it, so a thread takes 16 bytes (32 codes) of a row,
+// whose 8-code words decode to the pairs (c0, c4), (c1, c5), ... (bsq_decode.cuh), and the tokens'
+// values are brought to that order.  Chunks of 16 bytes lie exchanged within their line, by
+// the row, so that a fragment's reads fall in different banks.  CTAs begin at different steps:
+// when all asked for the same tokens' values at once, that held them up (14336 x 5120, 8 rows: 24
+// us against 19 at the time).  The groups' accumulators are added in their order through
+// shared memory, so results do not depend on timing.
 //
-// Measured (graph of calls on rotated weights): 4096 x 4096 MXFP4, one row 5.7 us; 14336 x 5120 NVFP4,
-// 1 / 8 / 16 rows 17 / 19 / 23 us; 64 rows by 128 MXFP4 experts of 2048 x 7168 83 us, 3.7 TB/s.
-// Without the multiplication those 14336 x 5120 take 12 us, without the loads 11.
+// Measured (a graph of calls on rotated weights): 4096 x 4096 MXFP4, one row 4.5 us; 14336 x 5120 NVFP4,
+// 1 / 8 / 16 / 32 / 64 rows 15 / 16 / 18 / 24 / 43 us (MXFP4 12 / 13 / 16 / 21 / 37), where the 256-row
+// tile kernel of bsq_linear_forward takes 50 (41); 64 rows by 128 MXFP4 experts of 2048 x 7168 81 us,
+// 3.7 TB/s.  Of those 14336 x 5120 a warp spends its time so: 1.7 us to the first copies' end of
+// asking, 1.5 until the first step is there, then at 0.93 instructions a cycle and SM quarter.
 #include <cuda_bf16.h>
 
 #include "bsq_decode.cuh"
@@ -49,11 +55,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// 16 bytes from global to shared memory, past L1 and without a register; a group per step.
+// Bytes from global to shared memory without a register, past L1 where they are 16; zeros if not `there`.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
-  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, bool there) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -75,7 +81,7 @@ struct Scales<BSQ_MXFP4> {
     c[0] = bytes * 0x00800080u + 126u * 0x00800080u;   // (b + 126) << 7 in both halves
     return bytes > 128u;
   }
-  static __device__ __forceinline__ uint32_t plain(uint32_t bytes, int, float) { return make_scale_e8m0(bytes).s2; }
+  static __device__ __forceinline__ uint32_t plain(uint32_t bytes, int, float) { return make_scale_e8m0(bytes & 0xFFu).s2; }
 };
 template <>
 struct Scales<BSQ_NVFP4> {
@@ -93,27 +99,36 @@ struct Scales<BSQ_NVFP4> {
   static __device__ __forceinline__ uint32_t plain(uint32_t bytes, int i, float ts) { return make_scale_nvfp4(bytes >> (8 * i), ts).s2; }
 };
 
-// MT: 16-row groups of W a CTA; NT: groups of 8 tokens per pass over W; STAGES: steps of 128 k
-// that a warp has in flight; WARPS of a CTA; CTAS an SM shall hold.  ALIGNED: K % 128 == 0 and
-// aligned scales, which then come by copies of a row's bytes of a step.
-template <int FMT, int MT, int NT, int STAGES, int WARPS, int CTAS, bool ALIGNED>
-__global__ void __launch_bounds__(WARPS * 32, CTAS) fp4_smallm_kernel(const Fp4SmallParams p) {
-  constexpr int kRows = 16 * MT, kPad = kRows + 4;   // the pitch keeps fragment writes free of bank conflicts
+// The warps that share a k: RW of them, one after the other in the CTA.
+template <int RW>
+__device__ __forceinline__ void group_sync(int group) {
+  if (RW == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(RW * 32) : "memory");
+}
+
+constexpr int kStepK = 256;             // k of a step: 128 bytes of a row of W, a whole cache line
+
+// MT: 16-row groups of W a warp; RW: warps beside one another in N; KW: in k; NT: groups of 8 tokens
+// per pass over W; STAGES: steps in flight; CTAS an SM shall hold.  ALIGNED: K % 256 == 0 and
+// scales to match, which are then copied once for the whole tile.
+template <int FMT, int MT, int RW, int KW, int NT, int STAGES, int CTAS, bool ALIGNED>
+__global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp4SmallParams p) {
+  constexpr int kThreads = RW * KW * 32;
+  constexpr int kWarpRows = 16 * MT, kRows = kWarpRows * RW, kPad = kRows + 4;   // the pitch keeps fragment writes free of bank conflicts
   constexpr int kCount = Scales<FMT>::kCount;
   constexpr int kShift = FMT == BSQ_NVFP4 ? 4 : 5;   // log2 of the elements of a scale
-  // a warp's step in shared memory: W (read back by the thread that copied it), the tokens' values, the
-  // rows' scales
-  constexpr int kX = 2 * MT * 512, kS = kX + NT * 2048, kStage = kS + (kRows * 4 * kCount + 15) / 16 * 16;
-  extern __shared__ __align__(16) uint8_t smem[];    // [WARPS][STAGES][kStage]; the partial sums in its place
+  constexpr int kX = kRows * 128, kStage = kX + NT * 8 * 512;   // a group's step: rows of W, tokens
+  extern __shared__ __align__(128) uint8_t smem[];   // [KW][STAGES][kStage], the tile's scales; the partial sums in the place of the first
   float (*red)[8][kPad] = reinterpret_cast<float (*)[8][kPad]>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = warp / RW, rw = warp % RW;
   const int g = lane >> 2, t = lane & 3;
   const int e = blockIdx.y;
   int r0 = 0, r1 = p.S, bad = 0;
   if (p.offsets) {
     r0 = e > 0 ? __ldg(p.offsets + e - 1) : 0;
     r1 = __ldg(p.offsets + e);
-    for (int i = tid; i < p.E; i += WARPS * 32) {
+    for (int i = tid; i < p.E; i += kThreads) {
       const int a = i > 0 ? __ldg(p.offsets + i - 1) : 0, b = __ldg(p.offsets + i);
       bad |= a < 0 || b < a || b > p.S;
     }
@@ -126,18 +141,61 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp4_smallm_kernel(const Fp4S
   const int rows_left = p.N - 1 - n0;
   const int64_t row0 = static_cast<int64_t>(e) * p.N + n0;
   const uint32_t wpitch = static_cast<uint32_t>(p.K) >> 1, spitch = static_cast<uint32_t>(p.K) >> kShift;
-  const uint8_t* wbase = p.w + row0 * wpitch + 16 * t;
+  const uint32_t tpitch = spitch + 16;               // of the scales in shared memory: rows fall in different banks
   const uint8_t* sbase = p.ws + row0 * spitch;
   const float ts = FMT == BSQ_NVFP4 ? __ldg(p.ts + e) : 0.f;
-  const uint8_t* ring = smem + warp * STAGES * kStage;
-  const uint32_t ring_at = smem_u32(ring);
-  const int steps = (p.K + 127) >> 7;
+  uint8_t* tile = smem + KW * STAGES * kStage;
+  const uint32_t ring = smem_u32(smem) + group * (STAGES * kStage);
+  const uint8_t* ring_ptr = smem + group * (STAGES * kStage);
+  const int steps = (p.K + kStepK - 1) / kStepK;
   // CTAs begin at different steps, so that they do not all ask for the same tokens' values at once
   const int turned = static_cast<int>(blockIdx.x * 5u) % steps;
 
+  // W is copied by the warp whose rows they are, eight lanes a row of a step, to the place of its
+  // chunk under the rows' exchange of chunks; the tokens' by all warps of the group.
+  const int wl = lane >> 3, wc = lane & 7;
+  const uint8_t* wsrc = p.w + row0 * wpitch + 16 * wc;
+  const uint32_t wdst = static_cast<uint32_t>(rw * kWarpRows + wl) * 128;
+
   for (int m0 = r0; m0 < r1; m0 += 8 * NT) {
-    const int left = r1 - m0;
-    const __nv_bfloat16* xbase = p.x + static_cast<int64_t>(m0) * p.K;
+    const int left = min(r1 - m0, 8 * NT);
+    const __nv_bfloat16* xsrc = p.x + static_cast<int64_t>(m0) * p.K + 8 * lane;
+    const auto fetch = [&](int turn, int slot) {
+      if (turn < steps) {
+        const int step = turn + turned < steps ? turn + turned : turn + turned - steps;
+        const uint32_t to = ring + slot * kStage;
+        const bool win = ALIGNED || kStepK * step + 32 * wc < p.K, xin = ALIGNED || kStepK * step + 8 * lane < p.K;
+#pragma unroll
+        for (int j = 0; j < 4 * MT; ++j) {
+          const int r = rw * kWarpRows + 4 * j + wl;
+          copy_async<16>(to + wdst + j * 512 + ((wc ^ (r & 7)) << 4), win ? wsrc + (static_cast<uint32_t>(min(r, rows_left)) * wpitch + 128u * step) : p.w, win);
+        }
+        for (int m = rw; m < left; m += RW)
+          copy_async<16>(to + kX + m * 512 + (lane >> 3) * 128 + (((lane & 7) ^ (2 * (lane >> 3) + (m & 1))) << 4),
+                         reinterpret_cast<const uint8_t*>(xin ? xsrc + (static_cast<int64_t>(m) * p.K + kStepK * step) : p.x), xin);
+      }
+      copy_commit();
+    };
+    if (ALIGNED && m0 == r0) {
+      // the tile's scales, in pieces of 16 or 8 bytes; a power of two of lanes a row
+      const int size = spitch & 15u ? 8 : 16, pieces = static_cast<int>(spitch) / size;
+      const int shift = pieces <= 4 ? 2 : pieces <= 8 ? 3 : pieces <= 16 ? 4 : 5;
+      for (int r = tid >> shift; r < kRows; r += kThreads >> shift) {
+        const uint8_t* src = sbase + static_cast<uint32_t>(min(r, rows_left)) * spitch;
+        const uint32_t dst = smem_u32(tile) + r * tpitch;
+        for (int i = tid & ((1 << shift) - 1); i < pieces; i += 1 << shift) {
+          if (size == 16) copy_async<16>(dst + 16 * i, src + 16 * i, true);
+          else copy_async<8>(dst + 8 * i, src + 8 * i, true);
+        }
+      }
+      copy_commit();
+    }
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) fetch(group + s * KW, s);
+    if (ALIGNED && m0 == r0) {
+      copy_wait<STAGES>();
+      __syncthreads();
+    }
     float acc[MT][NT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -146,108 +204,88 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp4_smallm_kernel(const Fp4S
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][j][c] = 0.f;
 
-    const auto fetch = [&](int turn, int slot) {
-      const uint32_t to = ring_at + slot * kStage;
-      if (turn < steps) {
-        const int step = turn + turned < steps ? turn + turned : turn + turned - steps;
-        if (ALIGNED || 128 * step + 32 * t < p.K) {     // K % 32 == 0: whole pieces of 32 codes
+    // Thread (g, t) takes the chunks 2 t and 2 t + 1 of a row: k = 64 t + 32 h of the step.
+    const uint32_t wat = static_cast<uint32_t>(rw * kWarpRows + g) * 128 + (((2 * t) ^ g) << 4);
+    uint32_t xat[NT];          // columns past the last token: any token, not stored
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i)
-            copy_async<16>(to + i * 512 + lane * 16, wbase + (static_cast<uint32_t>(min(8 * i + g, rows_left)) * wpitch + 64u * step));
-        }
-        // sixteen lanes a token: one's 16 eights of the step, to where the lanes that need them read
-#pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) {
-          const int m = 2 * i + (lane >> 4), q = (lane >> 2) & 3, c = lane & 3;
-          if (m < left && (ALIGNED || 128 * step + 32 * q < p.K))
-            copy_async<16>(to + kX + ((m >> 3) * 4 + c) * 512 + ((m & 7) * 4 + q) * 16,
-                           reinterpret_cast<const uint8_t*>(xbase + (static_cast<int64_t>(m) * p.K + 128 * step + 8 * (lane & 15))));
-        }
-        if (ALIGNED) {
-#pragma unroll
-          for (int i = 0; i < kRows; i += 32)
-            if (i + lane < kRows)
-              copy_async<4 * kCount>(to + kS + (i + lane) * 4 * kCount, sbase + (static_cast<uint32_t>(min(i + lane, rows_left)) * spitch + 4u * kCount * step));
-        }
-      }
-      copy_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(warp + s * WARPS, s);
+    for (int j = 0; j < NT; ++j) {
+      const int m = min(8 * j + g, left - 1);
+      xat[j] = kX + m * 512 + t * 128 + ((2 * t + (m & 1)) << 4);
+    }
     int slot = 0;
 #pragma unroll 1
-    for (int turn = warp; turn < steps; turn += WARPS) {
+    for (int turn = group; turn < steps; turn += KW) {
       const int step = turn + turned < steps ? turn + turned : turn + turned - steps;
-      const bool in = ALIGNED || 128 * step + 32 * t < p.K;
-      const uint8_t* from = ring + slot * kStage;
+      // the scales of both halves: byte (or pair) 2 t, 2 t + 1 of the row's
       uint32_t sv[MT][2];
-      if (!ALIGNED) {
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          const uint8_t* s = sbase + (static_cast<uint32_t>(min(8 * i + g, rows_left)) * spitch + kCount * (4 * step + t));
-          sv[i >> 1][i & 1] = Scales<FMT>::kOne;
-          if (in) sv[i >> 1][i & 1] = FMT == BSQ_NVFP4 ? __ldg(reinterpret_cast<const uint16_t*>(s)) : __ldg(s);
-        }
-      }
-      copy_wait<STAGES - 2>();
-      __syncwarp();          // tokens and scales were copied by other lanes
-      if (ALIGNED) {
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          const uint8_t* s = from + kS + (8 * i + g) * 4 * kCount + kCount * t;
-          sv[i >> 1][i & 1] = FMT == BSQ_NVFP4 ? *reinterpret_cast<const uint16_t*>(s) : *s;
-        }
-      }
-      Scales<FMT> f[MT][2];
-      bool slow = false;
-#pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1], ts);
-      slow = __any_sync(kFull, slow);
-      uint4 wv[MT][2];
 #pragma unroll
       for (int i = 0; i < 2 * MT; ++i) {
-        wv[i >> 1][i & 1] = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
-        if (!in) wv[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+        uint32_t& v = sv[i >> 1][i & 1];
+        const int r = rw * kWarpRows + 8 * i + g;
+        const uint32_t at = static_cast<uint32_t>(8 * step + 2 * t) * kCount;
+        if (ALIGNED) {
+          const uint8_t* s = tile + r * tpitch + at;
+          v = FMT == BSQ_NVFP4 ? *reinterpret_cast<const uint32_t*>(s) : *reinterpret_cast<const uint16_t*>(s);
+        } else {
+          const uint8_t* s = sbase + (static_cast<uint32_t>(min(r, rows_left)) * spitch + at);
+          v = Scales<FMT>::kOne * 0x01010101u;
+#pragma unroll
+          for (int b = 0; b < 2 * kCount; ++b)
+            if (at + b < spitch) v = (v & ~(0xFFu << (8 * b))) | (static_cast<uint32_t>(__ldg(s + b)) << (8 * b));
+        }
       }
-      const auto multiply = [&](auto is_slow) {
+      copy_wait<STAGES - 1>();
+      group_sync<RW>(group);         // what other lanes and warps copied is there
+      const uint8_t* from = ring_ptr + slot * kStage;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t xp[NT][4];      // in the order of the decoded pairs
+      for (int h = 0; h < 2; ++h) {
+        Scales<FMT> f[MT][2];
+        bool slow = false;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint4 v = *reinterpret_cast<const uint4*>(from + kX + (j * 4 + c) * 512 + lane * 16);
-            if (!in) v = make_uint4(0, 0, 0, 0);
-            unzip_pairs(v.x, v.z, xp[j][0], xp[j][1]);
-            unzip_pairs(v.y, v.w, xp[j][2], xp[j][3]);
-          }
+        for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), ts);
+        slow = __any_sync(kFull, slow);
+        uint4 wv[MT][2];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t a[2][4];
+        for (int i = 0; i < 2 * MT; ++i) wv[i >> 1][i & 1] = *reinterpret_cast<const uint4*>(from + ((wat ^ (h << 4)) + i * 1024));
+        const auto multiply = [&](auto is_slow) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              spread_e2m1x8(word(wv[i][q], c), a[q]);
-              const int s = kCount == 2 ? c >> 1 : 0;
-              if (decltype(is_slow)::value) {
-                const uint32_t plain = Scales<FMT>::plain(sv[i][q], s, ts);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) a[q][u] = bf16x2_mul(bf16x2_mul(a[q][u], kPow2_126x2), plain);
-              } else {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) a[q][u] = bf16x2_mul(a[q][u], f[i][q].c[s]);
-              }
-            }
+          for (int c = 0; c < 4; ++c) {
+            uint32_t xp[NT][4];      // in the order of the decoded pairs
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              mma_bf16(acc[i][j], a[0][0], a[1][0], a[0][1], a[1][1], xp[j][0], xp[j][1]);
-              mma_bf16(acc[i][j], a[0][2], a[1][2], a[0][3], a[1][3], xp[j][2], xp[j][3]);
+              const uint4 v = *reinterpret_cast<const uint4*>(from + (xat[j] ^ ((4 * h + c) << 4)));
+              unzip_pairs(v.x, v.z, xp[j][0], xp[j][1]);
+              unzip_pairs(v.y, v.w, xp[j][2], xp[j][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              uint32_t a[2][4];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                spread_e2m1x8(word(wv[i][q], c), a[q]);
+                const int s = kCount == 2 ? c >> 1 : 0;
+                if (decltype(is_slow)::value) {
+                  const uint32_t plain = Scales<FMT>::plain(sv[i][q] >> (8 * kCount * h), s, ts);
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) a[q][u] = bf16x2_mul(bf16x2_mul(a[q][u], kPow2_126x2), plain);
+                } else {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) a[q][u] = bf16x2_mul(a[q][u], f[i][q].c[s]);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                mma_bf16(acc[i][j], a[0][0], a[1][0], a[0][1], a[1][1], xp[j][0], xp[j][1]);
+                mma_bf16(acc[i][j], a[0][2], a[1][2], a[0][3], a[1][3], xp[j][2], xp[j][3]);
+              }
             }
           }
-        }
-      };
-      if (!slow) multiply(std::false_type{});
-      else multiply(std::true_type{});
-      __syncwarp();          // every lane has read the step before
-      fetch(turn + (STAGES - 1) * WARPS, slot == 0 ? STAGES - 1 : slot - 1);
+        };
+        if (!slow) multiply(std::false_type{});
+        else multiply(std::true_type{});
+      }
+      group_sync<RW>(group);         // every lane has read the step
+      fetch(turn + STAGES * KW, slot);
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
     copy_wait<0>();
@@ -257,17 +295,18 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp4_smallm_kernel(const Fp4S
       if (8 * j >= left) break;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        red[warp][2 * t][16 * i + g] = acc[i][j][0];
-        red[warp][2 * t + 1][16 * i + g] = acc[i][j][1];
-        red[warp][2 * t][16 * i + 8 + g] = acc[i][j][2];
-        red[warp][2 * t + 1][16 * i + 8 + g] = acc[i][j][3];
+        const int n = rw * kWarpRows + 16 * i + g;
+        red[group][2 * t][n] = acc[i][j][0];
+        red[group][2 * t + 1][n] = acc[i][j][1];
+        red[group][2 * t][n + 8] = acc[i][j][2];
+        red[group][2 * t + 1][n + 8] = acc[i][j][3];
       }
       __syncthreads();
-      for (int o = tid; o < 8 * kRows; o += WARPS * 32) {
+      for (int o = tid; o < 8 * kRows; o += kThreads) {
         const int m = o / kRows, n = o % kRows;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += red[w][m][n];
+        for (int w = 0; w < KW; ++w) s += red[w][m][n];
         if (8 * j + m < left && n <= rows_left) p.y[static_cast<int64_t>(m0 + 8 * j + m) * p.N + n0 + n] = __float2bfloat16_rn(s);
       }
       __syncthreads();
@@ -275,18 +314,21 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) fp4_smallm_kernel(const Fp4S
   }
 }
 
-template <int FMT, int MT, int NT, int STAGES, int WARPS, int CTAS>
+template <int FMT, int MT, int RW, int KW, int NT, int STAGES, int CTAS>
 int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
-  const dim3 grid(static_cast<unsigned>((a.N + 16 * MT - 1) / (16 * MT)), static_cast<unsigned>(a.offsets ? a.E : 1));
-  constexpr int kStage = 2 * MT * 512 + NT * 2048 + (16 * MT * 4 * Scales<FMT>::kCount + 15) / 16 * 16;
-  constexpr int kRing = WARPS * STAGES * kStage, kRed = WARPS * 8 * (16 * MT + 4) * 4;
-  constexpr int kSmem = kRing > kRed ? kRing : kRed;
-  const bool aligned = a.K % 128 == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & 7u) == 0;
-  const auto kernel = aligned ? fp4_smallm_kernel<FMT, MT, NT, STAGES, WARPS, CTAS, true> : fp4_smallm_kernel<FMT, MT, NT, STAGES, WARPS, CTAS, false>;
+  constexpr int kRows = 16 * MT * RW;
+  const dim3 grid(static_cast<unsigned>((a.N + kRows - 1) / kRows), static_cast<unsigned>(a.offsets ? a.E : 1));
+  constexpr int kRing = KW * STAGES * (kRows * 128 + NT * 8 * 512), kRed = KW * 8 * (kRows + 4) * 4;
+  static_assert(kRed <= kRing && kRing <= 224 * 1024, "shared memory");
+  const int64_t spitch = a.K / (FMT == BSQ_NVFP4 ? 16 : 32);
+  const int64_t with = kRing + kRows * (spitch + 16);
+  const bool aligned = a.K % kStepK == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & (spitch % 16 ? 7u : 15u)) == 0 && with <= 227 * 1024;
+  const int smem = aligned ? static_cast<int>(with) : kRing;
+  const auto kernel = aligned ? fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, true> : fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, false>;
   cudaError_t e = cudaSuccess;
-  if (kSmem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
-    kernel<<<grid, WARPS * 32, kSmem, a.stream>>>(p);
+    kernel<<<grid, RW * KW * 32, smem, a.stream>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) {
@@ -296,22 +338,34 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   return 0;
 }
 
+// The tile and the tokens of a pass by the number of rows; every limit with both sides measured, in
+// us.  Per expert the limits are on the average, since the counts are the device's:
+//   64 experts of 2816 x 2048 NVFP4   192 rows 60.7 with 8 tokens a pass, 65.4 with 16; 256: 64.6, 66.5;
+//                                     512: 80 with 16 (64-row tiles; 48-row 83); 1024: 107 (48-row 105), 125 with 32;
+//                                     2048: 174 with 16, 160 with 32
+//   32 experts of 2048 x 7168 MXFP4   96 rows 63 with 8 tokens, 73 with 16; 384: 109 in 64-row tiles, 103 in 48-row
+// Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 7.8 with 32
+// tokens a pass, 10.4 with 16; then 14336 x 5120 NVFP4, 8 rows 15.5 in 32-row tiles, 15.8 in
+// 96-row ones; 13 rows 18.3 in 32-row tiles, 17.8 in 96-row ones; 32 rows 24.4 in 48-row tiles, 25.4 in 96-row ones.
 template <int FMT>
 int launch_fmt(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   if (a.offsets) {
-    // an expert's rows on average: more than one pass over its W for the few that have more
-    if (a.S <= 2 * a.E) return launch_typed<FMT, 4, 1, 3, 4, 2>(p, a, msg);
-    return launch_typed<FMT, 4, 2, 2, 4, 2>(p, a, msg);
+    if (a.S <= 4 * a.E) return launch_typed<FMT, 3, 1, 4, 1, 1, 3>(p, a, msg);
+    if (a.S <= 8 * a.E) return launch_typed<FMT, 4, 1, 4, 2, 1, 3>(p, a, msg);
+    return a.S <= 16 * a.E ? launch_typed<FMT, 3, 1, 4, 2, 1, 3>(p, a, msg) : launch_typed<FMT, 3, 1, 4, 4, 1, 2>(p, a, msg);
   }
-  const bool narrow = a.N <= 32 * a.num_sms;
-  if (a.S <= 8) return narrow ? launch_typed<FMT, 2, 1, 3, 8, 2>(p, a, msg) : launch_typed<FMT, 6, 1, 3, 8, 1>(p, a, msg);
-  if (narrow && a.S > 16) return launch_typed<FMT, 2, 4, 2, 8, 1>(p, a, msg);
-  return narrow ? launch_typed<FMT, 2, 2, 2, 8, 2>(p, a, msg) : launch_typed<FMT, 6, 2, 2, 8, 1>(p, a, msg);
+  if (a.N <= 32 * a.num_sms) {
+    if (a.S <= 8) return launch_typed<FMT, 2, 1, 8, 1, 2, 1>(p, a, msg);
+    return a.S <= 16 ? launch_typed<FMT, 2, 1, 8, 2, 2, 1>(p, a, msg) : launch_typed<FMT, 2, 1, 8, 4, 1, 1>(p, a, msg);
+  }
+  if (a.S <= 8) return launch_typed<FMT, 2, 1, 4, 1, 2, 3>(p, a, msg);
+  return a.S <= 16 ? launch_typed<FMT, 2, 3, 4, 2, 2, 1>(p, a, msg) : launch_typed<FMT, 3, 1, 4, 4, 1, 2>(p, a, msg);
 }
 
 }  // namespace
 
-bool fp4_takes_smallm(const Fp4Args& a) { return a.S <= 16 || (a.S <= 64 && a.N <= 32 * a.num_sms); }
+// Beyond, the 256-row tile kernel (14336 x 5120 MXFP4: 64 rows 37 us here in two passes, 41.5 there).
+bool fp4_takes_smallm(const Fp4Args& a) { return a.S <= 64; }
 
 int launch_fp4_smallm(const Fp4Args& a, const char** msg) {
   Fp4SmallParams p;

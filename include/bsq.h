@@ -441,9 +441,8 @@ bsq_status bsq_combine_backward(const void* grad_out, const void* y, int64_t S, 
 /*
  * bsq_fp4_forward -- y[M][N] = X[M][K] deq(W)[N][K]^T of a BF16 X and a 4-bit W (BSQ_MXFP4 or
  * BSQ_NVFP4, K % 32 == 0, N % 8 == 0), dequantized by the rule above, accumulated in FP32 and
- * rounded once: for decoding.  Up to 16 rows (up to 64 while N <= 32 times the SMs) stream W
- * through a kernel of their own; more take bsq_linear_forward's.  y: bf16[M][N], fully written;
- * K == 0 gives zeros.  K <= 2^24.
+ * rounded once: for decoding.  Up to 64 rows stream W through a kernel of their own; more take
+ * bsq_linear_forward's.  y: bf16[M][N], fully written; K == 0 gives zeros.  K <= 2^24.
  */
 bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* w_data, const void* w_scale,
                            const float* w_tensor_scale, int64_t N, int64_t K, void* y, void* stream);
@@ -452,7 +451,7 @@ bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* 
  * bsq_fp4_grouped_forward -- that product per expert: rows [offsets[e-1] or 0, offsets[e]) against
  * W[e].  W: [E][N][K], w_tensor_scale f32[E]; offsets, rows past offsets[E-1] (never read or
  * written) and the limits on E are those of bsq_grouped_dgrad.  Any S, but made for decoding: an
- * expert's W is decoded again for every 8 or 16 of its rows.  K == 0 with S > 0 is unsupported.
+ * expert's W is decoded again for every 8 to 32 of its rows.  K == 0 with S > 0 is unsupported.
  */
 bsq_status bsq_fp4_grouped_forward(const void* x, int64_t S, int32_t w_fmt, const void* w_data, const void* w_scale,
                                    const float* w_tensor_scale, int64_t E, int64_t N, int64_t K, const int32_t* offsets,
