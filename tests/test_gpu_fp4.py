@@ -144,3 +144,30 @@ def test_empty():
     assert bsq.fp4_forward(torch.zeros((0, 128), dtype=BF16, device="cuda"), W).shape == (0, 64)
     Z = synth.Packed(synth.FMT_MXFP4, W.data[:, :, :0].contiguous(), W.scale[:, :, :0].contiguous(), None, 1, 64, 0)
     assert not bsq.fp4_forward(torch.zeros((3, 0), dtype=BF16, device="cuda"), Z).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,at", [(40, {0: 1, 31: 2, 32: 1, 39: 3}), (1024, {1023: 1}), (1024, {5: 9, 700: 1, 701: 1}), (300, {})])
+def test_few_rows_on_many_experts(fmt, E, at):
+    """Fewer rows than experts: only those that have any take part."""
+    N, K, used = 72, 288, sum(at.values())
+    W = synth.make_packed(fmt, E, N, K, 0.5, seed=E, device="cuda")
+    X = activations(max(used, 2), K, 3)
+    offs = synth.offsets_from_counts([at.get(e, 0) for e in range(E)])
+    out = torch.full((len(X), N), 7.0, dtype=BF16, device="cuda")
+    bsq.fp4_grouped_forward(X.cuda(), W, torch.from_numpy(offs).cuda(), out=out)
+    got, x, r0 = bf16_vals(out), bf16_vals(X), 0
+    assert (got[used:] == 7).all()
+    for e, c in at.items():
+        one = synth.Packed(fmt, W.data[e:e + 1].cpu(), W.scale[e:e + 1].cpu(), None if W.tensor_scale is None else W.tensor_scale[e:e + 1].cpu(), 1, N, K)
+        w = oracle_deq(one)[0]
+        close(got[r0:r0 + c], x[r0:r0 + c] @ w.T, x[r0:r0 + c], w, f"expert {e}")
+        r0 += c
+
+
+@pytest.mark.parametrize("offs", [[0, 1, 0, 1, 2], [0, 0, -1, 0, 0], [0, 0, 0, 0, 3], [5, 5, 5, 5, 5]])
+def test_bad_offsets_of_many_experts(offs):
+    W = synth.make_packed(synth.FMT_NVFP4, 5, 64, 256, 0.5, seed=1, device="cuda")
+    out = torch.full((2, 64), 7.0, dtype=BF16, device="cuda")
+    bsq.fp4_grouped_forward(activations(2, 256, 1).cuda(), W, torch.tensor(offs, dtype=torch.int32, device="cuda"), out=out)
+    assert bsq.get_device_error() == (bsq.BSQ_ERR_INVALID_ARG, 2) and (out == 7).all()
