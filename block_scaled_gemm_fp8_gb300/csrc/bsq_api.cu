@@ -245,6 +245,9 @@ bsq_status run_fp4(const char* what, bool grouped, const void* x, int64_t S, int
     return fail(BSQ_ERR_INVALID_ARG, "%s: scale not 2-byte or tensor_scale not 4-byte aligned", what);
   if (S * K > 0 && (!x || !aligned16(x))) return fail(BSQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", what);
   if (S * N > 0 && (!y || !aligned16(y))) return fail(BSQ_ERR_INVALID_ARG, "%s: output null or not 16-byte aligned", what);
+  const bool few = grouped || S <= bsq::kFp4Rows;      // else bsq_linear_forward's tile kernel
+  if (!few && E * N * K > 0 && !aligned16(w_scale))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: scale not 16-byte aligned (more than %d rows)", what, bsq::kFp4Rows);
   if (S == 0 || N == 0) return BSQ_OK;
   if (K == 0) {
     if (grouped) return fail(BSQ_ERR_UNSUPPORTED, "%s: K == 0 with S > 0 (rows to zero depend on offsets)", what);
@@ -256,7 +259,7 @@ bsq_status run_fp4(const char* what, bool grouped, const void* x, int64_t S, int
   if (st != BSQ_OK) return st;
   bsq::Fp4Args a{w_fmt, x, w, w_scale, ts, S, N, K, E, grouped ? offsets : nullptr, y, err, sms, static_cast<cudaStream_t>(stream)};
   const char* msg = "";
-  if (!grouped && !bsq::fp4_takes_smallm(a))
+  if (!few)
     return bsq_linear_forward(BSQ_BF16, x, nullptr, nullptr, S, w_fmt, w, w_scale, ts, N, K, y, stream);
   if (bsq::launch_fp4_smallm(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
   return BSQ_OK;

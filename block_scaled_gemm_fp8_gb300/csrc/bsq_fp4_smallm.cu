@@ -385,9 +385,6 @@ int launch_fmt(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
 
 }  // namespace
 
-// Beyond, the 256-row tile kernel (14336 x 5120 MXFP4: 64 rows 37 us here in two passes, 41.5 there).
-bool fp4_takes_smallm(const Fp4Args& a) { return a.S <= 64; }
-
 int launch_fp4_smallm(const Fp4Args& a, const char** msg) {
   Fp4SmallParams p;
   p.x = static_cast<const __nv_bfloat16*>(a.x);

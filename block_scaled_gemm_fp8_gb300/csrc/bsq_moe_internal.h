@@ -59,6 +59,10 @@ int launch_dispatch(const TokenArgs& a, const char** msg);
 int launch_combine(const TokenArgs& a, const char** msg);
 int launch_combine_backward(const TokenArgs& a, const char** msg);
 
+// A dense product of more rows takes bsq_linear_forward's 256-row tile kernel (14336 x 5120 MXFP4: 64 rows
+// 37 us in the few-rows kernel's two passes, 41.5 there; NVFP4 43 and 50).
+constexpr int kFp4Rows = 64;
+
 struct Fp4Args {
   int fmt;                 // BSQ_MXFP4 or BSQ_NVFP4
   const void* x;           // bf16 [S][K]
@@ -73,7 +77,5 @@ struct Fp4Args {
   cudaStream_t stream;
 };
 int launch_fp4_smallm(const Fp4Args& a, const char** msg);
-// Whether a dense product of these sizes takes the few-rows kernel (else bsq_linear_forward's).
-bool fp4_takes_smallm(const Fp4Args& a);
 
 }  // namespace bsq

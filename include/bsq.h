@@ -39,6 +39,8 @@
  *       BSQ_MXFP4          data u8  [batch][rows][cols/2]; scale u8 [batch][rows][cols/32]
  *       BSQ_NVFP4          data u8  [batch][rows][cols/2]; scale u8 (E4M3) [batch][rows][cols/16];
  *                          tensor_scale f32[batch]
+ *   - Beside the products stand a mixture layer's other operators: the router, the tokens'
+ *     way to their experts' rows and back, and products of few rows with 4-bit weights.
  *   - Alignment: data/scale base pointers 16-byte aligned; the row pitch of every
  *     TMA-read tensor a multiple of 16 bytes, i.e. N % 8 == 0 for grad_out, and
  *     K % 16 (both FP8 formats), K % 32 (MXFP4, NVFP4), K % 8 (BF16) for the packed operand;
@@ -413,7 +415,8 @@ bsq_status bsq_sort_experts(const int32_t* ids, int64_t T, int32_t k, int64_t E,
  * rows outside 0..S-1 are left out.  weights: f32[T][k] or NULL for 1.  Rows that no slot owns
  * are not written.  out or codes may be NULL; codes and scale come together.  1 <= k <= 32.
  * The gradient of x is bsq_combine of the rows' gradient with the same rows and weights, that of
- * the weights bsq_combine_backward's grad_weights with x in the place of grad_out.
+ * the weights bsq_combine_backward's grad_weights with x in the place of grad_out.  Here and
+ * in the calls below no output may overlap an input.
  */
 bsq_status bsq_dispatch(const void* x, int64_t T, int64_t K, const int32_t* rows, int32_t k, const float* weights, int64_t S,
                         void* out, void* codes, float* scale, void* stream);
@@ -443,6 +446,8 @@ bsq_status bsq_combine_backward(const void* grad_out, const void* y, int64_t S, 
  * BSQ_NVFP4, K % 32 == 0, N % 8 == 0), dequantized by the rule above, accumulated in FP32 and
  * rounded once: for decoding.  Up to 64 rows stream W through a kernel of their own; more take
  * bsq_linear_forward's.  y: bf16[M][N], fully written; K == 0 gives zeros.  K <= 2^24.
+ * Scales: any alignment for MXFP4, 2 bytes for NVFP4 (an expert's slice of a stacked W will do),
+ * and faster where K % 256 == 0 and they are 16-byte aligned; beyond 64 rows 16 bytes.
  */
 bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* w_data, const void* w_scale,
                            const float* w_tensor_scale, int64_t N, int64_t K, void* y, void* stream);

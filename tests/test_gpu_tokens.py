@@ -184,9 +184,8 @@ def test_far_rows():
     assert torch.equal(codes[S - 1], qc[0]) and torch.equal(scale[S - 2], qs[1])
     y = bsq.combine(out, rows.cuda()).cpu()
     assert torch.equal(y, (2 * x.float()).to(BF16))
-    out.zero_()
-    bsq.combine_backward(x.cuda(), out, rows.cuda(), grad_y=out)
-    assert torch.equal(out[S - 1].cpu(), x[0])
+    grad, _, _, gw = bsq.combine_backward(x.cuda(), out, rows.cuda())
+    assert torch.equal(grad[S - 1].cpu(), x[0]) and torch.equal(gw[0, 0], gw[0, 1])
 
 
 # ---------------------------------------------------------------- combine and its gradient
