@@ -8,9 +8,11 @@
 //
 // All but the sort are bound by HBM: a token's columns are read once, whatever k is, and a
 // token's codes are made once, since a weight only changes a block's scale.
+#include <atomic>
 #include <cuda_bf16.h>
 
 #include "bsq_e4m3.cuh"
+#include "bsq_internal.h"
 #include "bsq_lanes.cuh"
 #include "bsq_moe_internal.h"
 #include "bsq_ptx.cuh"
@@ -47,8 +49,8 @@ __device__ __forceinline__ int32_t count_slots(int32_t* mine, int e, bool in, ui
 // counters of its own, the counts become first places (over warps, CTAs through distributed
 // shared memory, then experts), and every slot's place is its expert's first plus its rank.
 // HELD: slots a lane holds in registers, 32 HELD a warp's run; 0: any run, read and counted twice.
-// Bound by latency: 16384 slots on 64 experts take 4.7 us, of which a launch and two barriers of
-// the cluster are 3.
+// Bound by latency: 64 slots on 64 experts 2.6 us, 16384 4.9, 32764 on 128 6.5; then by the
+// scattered stores of `slots`, of which an SM does a sector a cycle (131072 on 128 experts 12.9 us).
 template <int HELD>
 __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
                                                                       int64_t run, int ctas, int32_t* __restrict__ offsets,
@@ -127,9 +129,9 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
     if (rank == 0) offsets[tid] = upto;
     if (tid == E - 1) kept = upto;
   }
-  // the cluster's counts have been read: no CTA leaves before
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
+  // No CTA leaves before the cluster has read its counts: said here, waited for at the end.
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  __syncthreads();
 
   const auto place = [&](int64_t i, int e, int32_t at) {
     const int32_t row = known(e) ? base[e] + at : -1;
@@ -151,6 +153,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_experts_kernel(const int
   if (slots)
     for (int64_t i = static_cast<int64_t>(kept) + rank * (kSortWarps * 32) + tid; i < n; i += static_cast<int64_t>(ctas) * (kSortWarps * 32))
       slots[i] = -1;
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- rows of a token
@@ -378,32 +381,67 @@ __global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
 
 }  // namespace
 
-int launch_sort_experts(const SortArgs& a, const char** msg) {
-  // One CTA while a warp of it has few slots; then eight, up to which a cluster runs anywhere.
-  const int ctas = a.n <= 1024 ? 1 : 8;
-  // a warp's run, in whole warps of slots
-  int64_t run = ((a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
-  auto kernel = sort_experts_kernel<0>;
-  if (run <= 32) kernel = sort_experts_kernel<1>;
-  else if (run <= 64) kernel = sort_experts_kernel<2>;
-  else if (run <= 128) kernel = sort_experts_kernel<4>;
-  else if (run <= 256) kernel = sort_experts_kernel<8>;
-  const size_t smem = static_cast<size_t>(kSortWarps + 2) * a.E * 4;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
+namespace {
+
+struct SortLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  SortLaunch(int ctas, size_t smem, cudaStream_t stream) {
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortWarps * 32);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr = {};
+    cfg.stream = stream;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = ctas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = ctas > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, a.ids, a.n, a.E, run, ctas, a.offsets, a.rows, a.slots);
+  }
+};
+
+// Whether a cluster of 16 such CTAs fits this device, which is asked once.
+bool sixteen_fit() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    const size_t smem = static_cast<size_t>(kSortWarps + 2) * kMaxExperts * 4;
+    const auto kernel = sort_experts_kernel<16>;
+    const SortLaunch l(16, smem, nullptr);
+    int clusters = 0;
+    const bool asked = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess &&
+                       cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                       cudaOccupancyMaxActiveClusters(&clusters, kernel, &l.cfg) == cudaSuccess;
+    if (!asked) cudaGetLastError();
+    k = asked && clusters > 0 ? 1 : 2;
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k == 1;
+}
+
+}  // namespace
+
+int launch_sort_experts(const SortArgs& a, const char** msg) {
+  // One CTA while a warp of it has few slots, then eight (8192 on 64 experts: 4.6 us, with sixteen 4.9), then
+  // sixteen, where the device has a place for such a cluster (16384: 5.8 us with eight, 4.9 with
+  // sixteen; 131072 on 128: 21.6 and 12.9; 800000 on 256: 146 and 79).
+  const int ctas = a.n <= 1024 ? 1 : a.n <= 8192 || !sixteen_fit() ? 8 : 16;
+  // a warp's run, in whole warps of slots
+  const int64_t run = ((a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  auto kernel = sort_experts_kernel<0>;
+  if (run <= 32) kernel = sort_experts_kernel<1>;
+  else if (run <= 64) kernel = sort_experts_kernel<2>;
+  else if (run <= 128) kernel = sort_experts_kernel<4>;
+  else if (run <= 256) kernel = sort_experts_kernel<8>;
+  else if (run <= 512) kernel = sort_experts_kernel<16>;
+  const size_t smem = static_cast<size_t>(kSortWarps + 2) * a.E * 4;
+  cudaError_t e = cudaSuccess;
+  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) {
+    SortLaunch l(ctas, smem, a.stream);
+    e = cudaLaunchKernelEx(&l.cfg, kernel, a.ids, a.n, a.E, run, ctas, a.offsets, a.rows, a.slots);
   }
   if (e != cudaSuccess) {
     *msg = cudaGetErrorString(e);

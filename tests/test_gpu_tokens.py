@@ -46,7 +46,7 @@ def sorted_plain(ids, E):
 
 # ---------------------------------------------------------------- sort
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (7, 3, 5), (33, 2, 1024), (100, 32, 1000), (1024, 8, 128), (1025, 8, 64),
-                                   (5000, 4, 257), (16384, 8, 256), (40001, 8, 1024), (3, 5, 1), (131072, 1, 3)])
+                                   (5000, 4, 257), (16384, 8, 256), (40001, 8, 1024), (3, 5, 1), (131072, 1, 3), (1366, 6, 64), (2047, 8, 31), (8191, 8, 64), (30000, 8, 1024)])
 @pytest.mark.parametrize("bad", [0.0, 0.3])
 def test_sort(T, k, E, bad):
     ids = draw_ids(T, k, E, T + E, bad)
