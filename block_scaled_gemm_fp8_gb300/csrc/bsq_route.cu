@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_kernel(const T* __restrict
     const int e = lane * V + v;
     float s = l[v];
     nan |= s != s;
-    if (BIAS && e < E) s = (SOFTMAX ? s : sigmoid(s)) + __ldg(bias + e);
+    // a masked expert stays so: its sigmoid would be zero, above an expert's with a lower bias
+    if (BIAS && e < E) s = (SOFTMAX || s == -INFINITY ? s : sigmoid(s)) + __ldg(bias + e);
     key[v] = order_of(s);
     expert[v] = e;
   }

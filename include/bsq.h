@@ -375,7 +375,7 @@ typedef enum {
  *   weights  f32[T][k]: factor * softmax(logits)[id], or factor * sigmoid(logit[id]);
  *            renormalize != 0: factor times the softmax over the chosen logits alone, or the
  *            sigmoids divided by their sum over the chosen (zeros if that sum is zero)
- * An expert whose score is a NaN or minus infinity is not chosen; slots that are left over (a
+ * An expert whose logit or score is a NaN or minus infinity is not chosen; slots that are left over (a
  * token whose logits are all masked) get id -1 and weight 0.  A NaN among a token's logits
  * makes its weights NaN.
  * logits: dtype (bsq_dtype) [T][E]; bias: f32[E] or NULL.  1 <= k <= 32, k <= E <= 1024.

@@ -124,6 +124,20 @@ def test_route_and_gradient(gate, renorm, dtype, T, E, k):
     check(draw(T, E, dtype, T + E, coarse=dtype == BF16), k, gate, renorm, factor=2.5, seed=E)
 
 
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_a_bias_does_not_unmask(gate):
+    x = torch.linspace(-1, 1, 40).repeat(3, 1)
+    x[0, 3:] = -float("inf")                # three experts left of five slots
+    x[1] = -float("inf")
+    x[2, :34] = -float("inf")
+    bias = torch.full((40,), 9.0)
+    bias[[0, 1, 2, 34, 35, 36, 37, 38, 39]] = -9.0
+    ids, w = bsq.route(x.cuda(), 5, gate=gate, bias=bias.cuda())
+    assert ids.cpu().tolist() == [[2, 1, 0, -1, -1], [-1] * 5, [39, 38, 37, 36, 35]]
+    w = w.cpu()
+    assert not w[0, 3:].any() and not w[1].any() and (w[2] > 0).all() and (w[0, :3] > 0).all()
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 def test_bias_takes_part_in_the_choice_alone(renorm):
     x, bias = draw(64, 96, F32, 3), torch.randn(96, generator=torch.Generator().manual_seed(4))
