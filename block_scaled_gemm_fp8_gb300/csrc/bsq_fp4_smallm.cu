@@ -261,9 +261,11 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         Scales<FMT> f[MT][2];
+        // codes that are not there stay zeros when the tensor's scale is infinite
+        const float tsh = ALIGNED || kStepK * step + 64 * t + 32 * h < p.K ? ts : 0.f;
         bool slow = false;
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), ts);
+        for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
         slow = __any_sync(kFull, slow);
         uint4 wv[MT][2];
 #pragma unroll
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
                 spread_e2m1x8(word(wv[i][q], c), a[q]);
                 const int s = kCount == 2 ? c >> 1 : 0;
                 if (decltype(is_slow)::value) {
-                  const uint32_t plain = Scales<FMT>::plain(sv[i][q] >> (8 * kCount * h), s, ts);
+                  const uint32_t plain = Scales<FMT>::plain(sv[i][q] >> (8 * kCount * h), s, tsh);
 #pragma unroll
                   for (int u = 0; u < 4; ++u) a[q][u] = bf16x2_mul(bf16x2_mul(a[q][u], kPow2_126x2), plain);
                 } else {

@@ -84,6 +84,18 @@ def test_nan_scales_stay_in_their_rows(fmt):
     assert not np.isfinite(got[1]).any() and np.isfinite(np.delete(got[[0, 2]], 5, axis=1)).all()
 
 
+@pytest.mark.parametrize("M", [1, 16, 40])
+@pytest.mark.parametrize("K", [32, 96, 256, 288, 2080])
+def test_infinite_tensor_scale(M, K):
+    """Positive codes, scales and tokens: every sum is infinite, whatever lies behind the last column."""
+    W = synth.make_packed(synth.FMT_NVFP4, 1, 72, K, 0.5, seed=K, device="cpu")
+    W.data = (W.data & 0x77) | 0x11
+    W.scale = torch.full_like(W.scale.view(torch.uint8), 0x38)
+    W.tensor_scale = torch.tensor([float("inf")])
+    out = bsq.fp4_forward(torch.ones((M, K), dtype=BF16).cuda(), W.to("cuda"))
+    assert (out.float() == float("inf")).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("N,K,counts", [(64, 64, [1]), (72, 160, [0, 3, 0, 1]), (136, 1056, [8, 0, 9, 1, 17, 0, 0, 5]), (40, 2048, [0, 0, 64]),
                                         (264, 512, [33, 100, 0, 7]), (48, 96, [1] * 40), (512, 3104, [2, 1, 0, 1, 4, 1]), (64, 256, [0, 0, 0])])
