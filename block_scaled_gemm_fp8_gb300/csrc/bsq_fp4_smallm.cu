@@ -23,6 +23,7 @@
 // 3.7 TB/s.  Of those 14336 x 5120 a warp spends its time so: 1.7 us to the first copies' end of
 // asking, 1.5 until the first step is there, then at 0.93 instructions a cycle and SM quarter.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "bsq_decode.cuh"
 #include "bsq_moe_internal.h"
@@ -77,9 +78,14 @@ struct Scales<BSQ_MXFP4> {
   static constexpr int kCount = 1;
   static constexpr uint32_t kOne = 127;      // a scale of 1, for codes that are not there
   uint32_t c[1];
-  __device__ __forceinline__ bool set(uint32_t bytes, float) {
+  static constexpr uint32_t kLarge = 0x80808080u;    // a byte with its top bit: a scale of 2 or more
+  static __device__ __forceinline__ bool ordinary(float) { return true; }
+  __device__ __forceinline__ void set_ordinary(uint32_t bytes, float) {
     c[0] = bytes * 0x00800080u + 126u * 0x00800080u;   // (b + 126) << 7 in both halves
-    return bytes > 128u;
+  }
+  __device__ __forceinline__ bool set(uint32_t bytes, float ts) {
+    set_ordinary(bytes, ts);
+    return false;
   }
   static __device__ __forceinline__ uint32_t plain(uint32_t bytes, int, float) { return make_scale_e8m0(bytes & 0xFFu).s2; }
 };
@@ -88,6 +94,19 @@ struct Scales<BSQ_NVFP4> {
   static constexpr int kCount = 2;
   static constexpr uint32_t kOne = 0;
   uint32_t c[2];
+  static constexpr uint32_t kLarge = 0;
+  // A tensor scale for which no scale times 2^126 is infinite and every scale is zero, a NaN or a normal
+  // number: the product and its rounding may then take the 2^126 with them (64 experts of
+  // 2816 x 2048, 509 rows: 76.5 us against 79.5; 14336 x 5120, 13 rows: 16.5 against 16.8).
+  static __device__ __forceinline__ bool ordinary(float ts) { return fabsf(ts) <= 0x1p-7f && fabsf(ts) >= 0x1p-110f; }
+  __device__ __forceinline__ void set_ordinary(uint32_t bytes, float ts) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(bytes)));
+    const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    const float t = ts * 0x1p126f;
+    c[0] = pack_bf16x2(__float_as_uint(__fmul_rn(s.x, t)), __float_as_uint(__fmul_rn(s.x, t)));
+    c[1] = pack_bf16x2(__float_as_uint(__fmul_rn(s.y, t)), __float_as_uint(__fmul_rn(s.y, t)));
+  }
   __device__ __forceinline__ bool set(uint32_t bytes, float ts) {
     const uint32_t s2 = pack_bf16x2(__float_as_uint(__fmul_rn(e4m3_to_f32(bytes), ts)), __float_as_uint(__fmul_rn(e4m3_to_f32(bytes >> 8), ts)));
     const uint32_t c2 = bf16x2_mul(s2, kPow2_126x2);
@@ -165,6 +184,7 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
   const uint32_t tpitch = spitch + 16;               // of the scales in shared memory: rows fall in different banks
   const uint8_t* sbase = p.ws + row0 * spitch;
   const float ts = FMT == BSQ_NVFP4 ? __ldg(p.ts + e) : 0.f;
+  const bool ordinary = Scales<FMT>::ordinary(ts);
   uint8_t* tile = smem + KW * STAGES * kStage;
   const uint32_t ring = smem_u32(smem) + group * (STAGES * kStage);
   const uint8_t* ring_ptr = smem + group * (STAGES * kStage);
@@ -258,15 +278,24 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
       copy_wait<STAGES - 1>();
       group_sync<RW>(group);         // what other lanes and warps copied is there
       const uint8_t* from = ring_ptr + slot * kStage;
+      uint32_t large = 0;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) large |= sv[i >> 1][i & 1];
+      bool slow = Scales<FMT>::kLarge && __any_sync(kFull, large & Scales<FMT>::kLarge);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         Scales<FMT> f[MT][2];
         // codes that are not there stay zeros when the tensor's scale is infinite
         const float tsh = ALIGNED || kStepK * step + 64 * t + 32 * h < p.K ? ts : 0.f;
-        bool slow = false;
+        if (ordinary) {
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
-        slow = __any_sync(kFull, slow);
+          for (int i = 0; i < 2 * MT; ++i) f[i >> 1][i & 1].set_ordinary(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
+        } else {
+          slow = false;
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
+          slow = __any_sync(kFull, slow);
+        }
         uint4 wv[MT][2];
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) wv[i >> 1][i & 1] = *reinterpret_cast<const uint4*>(from + ((wat ^ (h << 4)) + i * 1024));

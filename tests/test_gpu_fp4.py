@@ -84,6 +84,39 @@ def test_nan_scales_stay_in_their_rows(fmt):
     assert not np.isfinite(got[1]).any() and np.isfinite(np.delete(got[[0, 2]], 5, axis=1)).all()
 
 
+@pytest.mark.parametrize("ts", [2.0 ** -7, -(2.0 ** -7), 2.0 ** -7 * (1 + 2.0 ** -23), 2.0 ** -110, 2.0 ** -110 * (1 - 2.0 ** -24), 0.0, -3e-5, 2.0 ** 116])
+@pytest.mark.parametrize("K", [512, 288])
+def test_tensor_scales_at_which_the_decoding_changes(ts, K):
+    """Every code under every block scale, bit for bit, on both sides of each limit."""
+    N = 72
+    W = synth.random_codes(synth.FMT_NVFP4, 1, N, K, seed=K, device="cpu")
+    c = torch.arange(W.scale.numel(), dtype=torch.int64) * 7 % 256
+    c[(c & 0x7F) == 0x7F] = 1
+    W.scale, W.tensor_scale = c.to(torch.uint8).view(W.scale.shape), torch.tensor([ts], dtype=torch.float32)
+    want = oracle_deq(W)[0]
+    assert np.array_equal(bf16_vals(bsq.dequant(W.to("cuda")))[0], want) and np.isfinite(want).all()
+    for k0 in range(0, K, 32):
+        X = torch.zeros((32, K), dtype=BF16)
+        X[torch.arange(32), k0 + torch.arange(32)] = 1
+        assert np.array_equal(bf16_vals(bsq.fp4_forward(X.cuda(), W.to("cuda"))), want[:, k0:k0 + 32].T)
+
+
+@pytest.mark.parametrize("byte", [0, 1, 2, 126, 127, 128, 129, 200, 251])
+@pytest.mark.parametrize("K", [512, 288])
+def test_block_scales_at_which_the_decoding_changes(byte, K):
+    N = 72
+    W = synth.random_codes(synth.FMT_MXFP4, 1, N, K, seed=K, device="cpu")
+    b = torch.full(W.scale.shape, 120, dtype=torch.uint8)
+    b.view(-1)[::5] = byte
+    W.scale = b
+    want = oracle_deq(W)[0]
+    assert np.isfinite(want).all()
+    for k0 in range(0, K, 32):
+        X = torch.zeros((32, K), dtype=BF16)
+        X[torch.arange(32), k0 + torch.arange(32)] = 1
+        assert np.array_equal(bf16_vals(bsq.fp4_forward(X.cuda(), W.to("cuda"))), want[:, k0:k0 + 32].T)
+
+
 @pytest.mark.parametrize("M", [1, 16, 40])
 @pytest.mark.parametrize("K", [32, 96, 256, 288, 2080])
 def test_infinite_tensor_scale(M, K):
