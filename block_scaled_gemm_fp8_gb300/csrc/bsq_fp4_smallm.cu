@@ -1,7 +1,7 @@
 // bsq_fp4_smallm.cu -- products of a few BF16 token rows with 4-bit weights (decode), dense and
 // per expert:  y[m, n] = sum_k x[m, k] deq(W)[n, k],  deq = RNE_bf16(code * RNE_bf16(scale)).
 //
-// Bound by the instructions that decode W: about 93 for 1024 codes of a warp, 36 of them masks on
+// Bound by the instructions that decode W: about 93 for 1024 MXFP4 codes of a warp, 36 of them masks on
 // a pipe that takes one every other cycle.  A CTA owns some rows of W (columns of y) and the
 // whole contraction; RW warps beside one another in N and KW in k, whose groups take steps of
 // 256 k in turn, each with a ring of steps in shared memory that asynchronous copies fill.  256 k
@@ -17,11 +17,11 @@
 // us against 19 at the time).  The groups' accumulators are added in their order through
 // shared memory, so results do not depend on timing.
 //
-// Measured (a graph of calls on rotated weights): 4096 x 4096 MXFP4, one row 4.5 us; 14336 x 5120 NVFP4,
-// 1 / 8 / 16 / 32 / 64 rows 15 / 16 / 18 / 24 / 43 us (MXFP4 12 / 13 / 16 / 21 / 37), where the 256-row
-// tile kernel of bsq_linear_forward takes 50 (41); 64 rows by 128 MXFP4 experts of 2048 x 7168 81 us,
-// 3.7 TB/s.  Of those 14336 x 5120 a warp spends its time so: 1.7 us to the first copies' end of
-// asking, 1.5 until the first step is there, then at 0.93 instructions a cycle and SM quarter.
+// Measured (a graph of calls on rotated weights beyond L2): 4096 x 4096 MXFP4, one row 5.6 us; 14336 x 5120 NVFP4,
+// 1 / 8 / 16 / 32 / 64 rows 14.9 / 15.1 / 17.7 / 24.4 / 42 us (MXFP4 13.2 / 13.6 / 16.1 / 22.3 / 39.8); 64 rows
+// by 128 MXFP4 experts of 2048 x 7168 81 us, 3.8 TB/s; 512 by 64 NVFP4 experts of 2816 x 2048 80 us.
+// Of those 14336 x 5120 a warp spends its time so: 1.7 us to the first copies' end of asking, 1.5
+// until the first step is there, then the instructions.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -78,14 +78,11 @@ struct Scales<BSQ_MXFP4> {
   static constexpr int kCount = 1;
   static constexpr uint32_t kOne = 127;      // a scale of 1, for codes that are not there
   uint32_t c[1];
-  static constexpr uint32_t kLarge = 0x80808080u;    // a byte with its top bit: a scale of 2 or more
-  static __device__ __forceinline__ bool ordinary(float) { return true; }
-  __device__ __forceinline__ void set_ordinary(uint32_t bytes, float) {
+  static __device__ __forceinline__ bool ordinary(float) { return false; }
+  __device__ __forceinline__ void set_ordinary(uint32_t, float) {}
+  __device__ __forceinline__ bool set(uint32_t bytes, float) {
     c[0] = bytes * 0x00800080u + 126u * 0x00800080u;   // (b + 126) << 7 in both halves
-  }
-  __device__ __forceinline__ bool set(uint32_t bytes, float ts) {
-    set_ordinary(bytes, ts);
-    return false;
+    return bytes > 128u;
   }
   static __device__ __forceinline__ uint32_t plain(uint32_t bytes, int, float) { return make_scale_e8m0(bytes & 0xFFu).s2; }
 };
@@ -94,10 +91,9 @@ struct Scales<BSQ_NVFP4> {
   static constexpr int kCount = 2;
   static constexpr uint32_t kOne = 0;
   uint32_t c[2];
-  static constexpr uint32_t kLarge = 0;
   // A tensor scale for which no scale times 2^126 is infinite and every scale is zero, a NaN or a normal
   // number: the product and its rounding may then take the 2^126 with them (64 experts of
-  // 2816 x 2048, 509 rows: 76.5 us against 79.5; 14336 x 5120, 13 rows: 16.5 against 16.8).
+  // 2816 x 2048, 512 rows: 79.7 us against 81.4; 14336 x 5120, 13 rows: 17.5 against 17.8).
   static __device__ __forceinline__ bool ordinary(float ts) { return fabsf(ts) <= 0x1p-7f && fabsf(ts) >= 0x1p-110f; }
   __device__ __forceinline__ void set_ordinary(uint32_t bytes, float ts) {
     uint32_t h2;
@@ -278,22 +274,19 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
       copy_wait<STAGES - 1>();
       group_sync<RW>(group);         // what other lanes and warps copied is there
       const uint8_t* from = ring_ptr + slot * kStage;
-      uint32_t large = 0;
-#pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) large |= sv[i >> 1][i & 1];
-      bool slow = Scales<FMT>::kLarge && __any_sync(kFull, large & Scales<FMT>::kLarge);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         Scales<FMT> f[MT][2];
         // codes that are not there stay zeros when the tensor's scale is infinite
         const float tsh = ALIGNED || kStepK * step + 64 * t + 32 * h < p.K ? ts : 0.f;
+        const auto scale_bytes = [&](int i) { return sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu); };
+        bool slow = false;
         if (ordinary) {
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) f[i >> 1][i & 1].set_ordinary(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
+          for (int i = 0; i < 2 * MT; ++i) f[i >> 1][i & 1].set_ordinary(scale_bytes(i), tsh);
         } else {
-          slow = false;
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu), tsh);
+          for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(scale_bytes(i), tsh);
           slow = __any_sync(kFull, slow);
         }
         uint4 wv[MT][2];
@@ -392,13 +385,13 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
 
 // The tile and the tokens of a pass by the number of rows; every limit with both sides measured, in
 // us.  Per expert the limits are on the average, since the counts are the device's:
-//   64 experts of 2816 x 2048 NVFP4   192 rows 60.7 with 8 tokens a pass, 65.4 with 16; 256: 64.6, 66.5;
-//                                     512: 80 with 16 (64-row tiles; 48-row 83); 1024: 107 (48-row 105), 125 with 32;
-//                                     2048: 174 with 16, 160 with 32
-//   32 experts of 2048 x 7168 MXFP4   96 rows 63 with 8 tokens, 73 with 16; 384: 109 in 64-row tiles, 103 in 48-row
-// Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 7.8 with 32
-// tokens a pass, 10.4 with 16; then 14336 x 5120 NVFP4, 8 rows 15.5 in 32-row tiles, 15.8 in
-// 96-row ones; 13 rows 18.3 in 32-row tiles, 17.8 in 96-row ones; 32 rows 24.4 in 48-row tiles, 25.4 in 96-row ones.
+//   64 experts of 2816 x 2048 NVFP4   256 rows 62.5 with 8 tokens a pass, 66.5 with 16; 512: 84.6, 79.7 (64-row
+//                                     tiles; 48-row 82.6); 1024: 103 in 48-row tiles, 105 in 64-row ones, 126
+//                                     with 32 tokens; 2048: 170 with 16, 161 with 32
+//   32 experts of 2048 x 7168 MXFP4   96 rows 63 with 8 tokens, 74 with 16; 384: 109 in 64-row tiles, 104 in 48-row
+// Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 8.6 with 32
+// tokens a pass, 10.3 with 16; then 14336 x 5120 NVFP4, 8 rows 15.1 in 32-row tiles, 17.1 in
+// 96-row ones; 13 rows 21.9 in 32-row tiles, 17.5 in 96-row ones; 32 rows 24.4 in 48-row tiles, 30.2 in 96-row ones.
 template <int FMT>
 int launch_fmt(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   if (a.offsets) {

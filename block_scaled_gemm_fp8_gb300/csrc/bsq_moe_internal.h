@@ -60,7 +60,7 @@ int launch_combine(const TokenArgs& a, const char** msg);
 int launch_combine_backward(const TokenArgs& a, const char** msg);
 
 // A dense product of more rows takes bsq_linear_forward's 256-row tile kernel (14336 x 5120 MXFP4: 64 rows
-// 37 us in the few-rows kernel's two passes, 41.5 there; NVFP4 43 and 50).
+// 38 us in the few-rows kernel's two passes, 65 there 42; NVFP4 39.5 and 46).
 constexpr int kFp4Rows = 64;
 
 struct Fp4Args {
