@@ -241,8 +241,8 @@ bsq_status run_fp4(const char* what, bool grouped, const void* x, int64_t S, int
   if (st != BSQ_OK) return st;
   if (K % 32) return fail(BSQ_ERR_UNSUPPORTED, "%s: K %% 32 != 0 (packed row pitch must be 16 bytes)", what);
   if (N % 8) return fail(BSQ_ERR_UNSUPPORTED, "%s: N %% 8 != 0 (Y row pitch must be 16 bytes)", what);
-  if (E * N * K > 0 && ((reinterpret_cast<uintptr_t>(w_scale) & 1u) || !aligned4(ts)))
-    return fail(BSQ_ERR_INVALID_ARG, "%s: scale not 2-byte or tensor_scale not 4-byte aligned", what);
+  if (E * N * K > 0 && ((w_fmt == BSQ_NVFP4 && (reinterpret_cast<uintptr_t>(w_scale) & 1u)) || !aligned4(ts)))
+    return fail(BSQ_ERR_INVALID_ARG, "%s: NVFP4 scale not 2-byte or tensor_scale not 4-byte aligned", what);
   if (S * K > 0 && (!x || !aligned16(x))) return fail(BSQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", what);
   if (S * N > 0 && (!y || !aligned16(y))) return fail(BSQ_ERR_INVALID_ARG, "%s: output null or not 16-byte aligned", what);
   const bool few = grouped || S <= bsq::kFp4Rows;      // else bsq_linear_forward's tile kernel

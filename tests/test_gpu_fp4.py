@@ -117,6 +117,20 @@ def test_block_scales_at_which_the_decoding_changes(byte, K):
         assert np.array_equal(bf16_vals(bsq.fp4_forward(X.cuda(), W.to("cuda"))), want[:, k0:k0 + 32].T)
 
 
+@pytest.mark.parametrize("fmt,shift", [(synth.FMT_MXFP4, 1), (synth.FMT_MXFP4, 2), (synth.FMT_MXFP4, 8), (synth.FMT_NVFP4, 2), (synth.FMT_NVFP4, 8)])
+@pytest.mark.parametrize("K", [512, 288])
+def test_scales_of_any_alignment(fmt, shift, K):
+    W, X = synth.make_packed(fmt, 1, 72, K, 0.5, seed=K, device="cpu").to("cuda"), activations(9, K, 3).cuda()
+    want = bsq.fp4_forward(X, W)
+    buffer = torch.zeros(W.scale.numel() + 32, dtype=torch.uint8, device="cuda")
+    moved = buffer[shift:shift + W.scale.numel()].view(W.scale.shape)
+    moved.copy_(W.scale.view(torch.uint8))
+    W.scale = moved
+    assert moved.data_ptr() % 16 == shift and torch.equal(bsq.fp4_forward(X, W), want)
+    offsets = torch.tensor([9], dtype=torch.int32, device="cuda")
+    assert torch.equal(bsq.fp4_grouped_forward(X, W, offsets), bsq.fp4_grouped_forward(X, W.__class__(fmt, W.data, moved.clone(), W.tensor_scale, 1, 72, K), offsets))
+
+
 @pytest.mark.parametrize("M", [1, 16, 40])
 @pytest.mark.parametrize("K", [32, 96, 256, 288, 2080])
 def test_infinite_tensor_scale(M, K):

@@ -106,7 +106,7 @@ def test_fp4(L, grouped):
     assert call(x=None) == INVALID and call(x=FAKE + 8) == INVALID and call(w=None) == INVALID and call(w=FAKE + 8) == INVALID
     assert call(ws=None) == INVALID and call(fmt=3, ts=None) == INVALID and call(fmt=3, ts=FAKE + 2) == INVALID and call(fmt=3, ws=FAKE + 1) == INVALID
     assert call(y=None) == INVALID and call(y=FAKE + 8) == INVALID
-    assert call(M=0, x=None, y=None) == OK and call(N=0, y=None, w=None, ws=None) == OK
+    assert call(M=0, ws=FAKE + 1) == OK and call(M=0, x=None, y=None) == OK and call(N=0, y=None, w=None, ws=None) == OK
     if not grouped:
         assert call(M=65, ws=FAKE + 8) == INVALID              # the tile kernel's alignment
     if grouped:
