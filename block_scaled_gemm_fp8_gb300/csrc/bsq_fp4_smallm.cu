@@ -385,17 +385,18 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
 
 // The tile and the tokens of a pass by the number of rows; every limit with both sides measured, in
 // us.  Per expert the limits are on the average, since the counts are the device's:
-//   64 experts of 2816 x 2048 NVFP4   256 rows 62.5 with 8 tokens a pass, 66.5 with 16; 512: 84.6, 79.7 (64-row
+//   64 experts of 2816 x 2048 NVFP4   320 rows 63.6 with 8 tokens a pass, 69.2 with 16; 384: 70.4, 71.1; 512: 84.6, 79.7 (64-row
 //                                     tiles; 48-row 82.6); 1024: 103 in 48-row tiles, 105 in 64-row ones, 126
 //                                     with 32 tokens; 2048: 170 with 16, 161 with 32
-//   32 experts of 2048 x 7168 MXFP4   96 rows 63 with 8 tokens, 74 with 16; 384: 109 in 64-row tiles, 104 in 48-row
+//   32 experts of 2048 x 7168 MXFP4   160 rows 77 with 8 tokens, 86 with 16; 384: 109 in 64-row tiles, 104 in 48-row
+//   (128 experts of 1024 x 2048 would take 16 from 4 rows an expert: MXFP4 640 rows 67 with 8, 59 with 16)
 // Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 8.6 with 32
 // tokens a pass, 10.3 with 16; then 14336 x 5120 NVFP4, 8 rows 15.1 in 32-row tiles, 17.1 in
 // 96-row ones; 13 rows 21.9 in 32-row tiles, 17.5 in 96-row ones; 32 rows 24.4 in 48-row tiles, 30.2 in 96-row ones.
 template <int FMT>
 int launch_fmt(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   if (a.offsets) {
-    if (a.S <= 4 * a.E) return launch_typed<FMT, 3, 1, 4, 1, 1, 3>(p, a, msg);
+    if (a.S <= 5 * a.E) return launch_typed<FMT, 3, 1, 4, 1, 1, 3>(p, a, msg);
     if (a.S <= 8 * a.E) return launch_typed<FMT, 4, 1, 4, 2, 1, 3>(p, a, msg);
     return a.S <= 16 * a.E ? launch_typed<FMT, 3, 1, 4, 2, 1, 3>(p, a, msg) : launch_typed<FMT, 3, 1, 4, 4, 1, 2>(p, a, msg);
   }
