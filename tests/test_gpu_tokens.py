@@ -279,3 +279,28 @@ def test_empty_calls():
     assert y.shape == (4, 64) and not y.any()
     gw = bsq.combine_backward(z(4, 64), z(0, 64), torch.zeros((4, 2), dtype=I32, device="cuda"))[3]
     assert gw.shape == (4, 2) and not gw.any()
+
+
+def test_large_sorts_side_by_side():
+    """Clusters of sixteen CTAs, captured in two graphs that run on two streams at once, on other slots than they were captured with."""
+    held, graphs, outs = [], [], []
+    for s in range(2):
+        held.append(draw_ids(3000, 8, 256, s, 0.1).cuda())
+        bsq.sort_experts(held[s], 256)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[s]):
+            outs.append([bsq.sort_experts(held[s], 256) for _ in range(20)])
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    new = [draw_ids(3000, 8, 256, 7 + s, 0.1) for s in range(2)]
+    for s in range(2):
+        held[s].copy_(new[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        with torch.cuda.stream(side[s]):
+            graphs[s].replay()
+    torch.cuda.synchronize()
+    for s in range(2):
+        want = sorted_plain(new[s], 256)
+        for got in outs[s]:
+            assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
