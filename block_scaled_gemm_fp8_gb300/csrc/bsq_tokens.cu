@@ -9,7 +9,7 @@
 // All but the sort are bound by HBM: a token's columns are read once, whatever k is, and a
 // token's codes are made once, since a weight only changes a block's scale.  Dispatch of 4096
 // tokens of 2048 to four rows each, as BF16 and E4M3: 17.3 us, 6.8 TB/s; combine of eight rows of 7168
-// for 8191 tokens 155.6 us, 6.8 TB/s; of four of 2816 for 4096 tokens 21.6, its gradients 42.1 (6.1).
+// for 8191 tokens 153 us, 6.9 TB/s; of four of 2816 for 4096 tokens 20.7, its gradients 40.0 (6.4).
 #include <atomic>
 #include <cuda_bf16.h>
 
@@ -184,7 +184,7 @@ __device__ __forceinline__ float block_amax16(const Eight<__nv_bfloat16>& v) {
   return block_amax(m);
 }
 
-constexpr int kThreadsT = 256;
+constexpr int kThreadsT = 128;
 constexpr int kPieces = 2;       // pieces of 256 columns (eight a lane) per warp
 
 template <bool BF16, bool E4M3>
@@ -284,13 +284,17 @@ __global__ void __launch_bounds__(kThreadsT) combine_kernel(const __nv_bfloat16*
   }
 }
 
-// WPT warps of a CTA share a token: 1 with tokens enough to fill the GPU, up to 8.
+// Small CTAs, whose warps end at about the same time (4096 tokens of four rows of 2816, four warps a token: 41.8 us
+// in CTAs of eight warps, 40.4 in CTAs of four; the weights' gradient alone 23.4 and 21.4).
+constexpr int backward_warps(int wpt) { return wpt > kThreadsT / 32 ? wpt : kThreadsT / 32; }
+
+// WPT warps of a CTA share a token: 2 with tokens enough to fill the GPU, else 8.
 template <bool BF16, bool E4M3, bool DOT, int WPT>
-__global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
+__global__ void __launch_bounds__(backward_warps(WPT) * 32) combine_backward_kernel(
     const __nv_bfloat16* __restrict__ g, const __nv_bfloat16* __restrict__ y, int64_t tokens, int64_t S, int cols, int nblocks,
     const int32_t* __restrict__ rows, int k, const float* __restrict__ weights, __nv_bfloat16* __restrict__ out,
     uint8_t* __restrict__ codes, float* __restrict__ scale, float* __restrict__ grad_weights) {
-  constexpr int kWarps = kThreadsT / 32, kTokens = kWarps / WPT, G = kTogether, U = 2;
+  constexpr int kWarps = backward_warps(WPT), kTokens = kWarps / WPT, G = kTogether, U = 2;
   __shared__ float part[kWarps][G];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t own = static_cast<int64_t>(blockIdx.x) * kTokens + warp / WPT;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kThreadsT) combine_backward_kernel(
           for (int i = 0; i < WPT; ++i) sum += part[warp + i][lane];
           grad_weights[t * k + j0 + lane] = sum;
         }
-        __syncthreads();
+        if (j0 + G < k) __syncthreads();
       } else if (there && lane == 0) {
 #pragma unroll
         for (int u = 0; u < G; ++u)
@@ -472,15 +476,18 @@ int launch_dispatch(const TokenArgs& a, const char** msg) {
 }
 
 int launch_combine(const TokenArgs& a, const char** msg) {
-  // two pieces a warp: 8191 tokens of eight rows of 7168 155 us, with one 175, with four 160
-  constexpr int U = 2;
-  const int segs = static_cast<int>((a.cols + 256 * U - 1) / (256 * U));
+  // Two pieces a warp (8191 tokens of eight rows of 7168 153 us, with one 170), four where there are many
+  // tokens whose last piece of 1024 columns is more than half full (4096 of four of 2816: 20.7 us,
+  // with two 21.4; 1300 of eight of 4096: 18.5, with two 17.0; 16 of four of 2816: 2.6, with two 2.3).
+  const bool four = a.T >= 16ll * a.num_sms && (a.cols - 1) % 1024 >= 512;
+  const int segs = static_cast<int>(four ? (a.cols + 1023) / 1024 : (a.cols + 511) / 512);
   const int64_t grid = (a.T * segs + kThreadsT / 32 - 1) / (kThreadsT / 32);
   if (grid > INT32_MAX) {
     *msg = "too many blocks";
     return -1;
   }
-  combine_kernel<U><<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
+  const auto kernel = four ? combine_kernel<4> : combine_kernel<2>;
+  kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
       static_cast<const __nv_bfloat16*>(a.y), a.T, a.S, static_cast<int>(a.cols), segs, a.rows, a.k, a.weights,
       static_cast<__nv_bfloat16*>(a.out));
   return last_error(msg);
@@ -488,11 +495,13 @@ int launch_combine(const TokenArgs& a, const char** msg) {
 
 int launch_combine_backward(const TokenArgs& a, const char** msg) {
   const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
-  // 4096 tokens of four rows of 2816: four warps a token 42.7 us, one 49, eight 44.6
-  const int wpt = a.T >= 64ll * a.num_sms ? 1 : a.T >= 32ll * a.num_sms ? 2 : a.T >= 16ll * a.num_sms ? 4 : 8;
-  const int64_t grid = (a.T * wpt + kThreadsT / 32 - 1) / (kThreadsT / 32);
+  // four rows of 2816: 450 tokens 5.2 us with eight warps a token, 6.5 with two; 700: 7.3 and 7.1; 4096: 45 and 40.9
+  // (with one 44.1, with four 42.3)
+  const int wpt = a.T >= 4ll * a.num_sms ? 2 : 8;
+  const int warps = backward_warps(wpt);
+  const int64_t grid = (a.T * wpt + warps - 1) / warps;
   const auto go = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(grid), kThreadsT, 0, a.stream>>>(
+    kernel<<<static_cast<unsigned>(grid), warps * 32, 0, a.stream>>>(
         static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.y), a.T, a.S, cols, nb, a.rows, a.k,
         a.weights, static_cast<__nv_bfloat16*>(a.out), static_cast<uint8_t*>(a.codes), a.scale, a.grad_weights);
   };
@@ -510,9 +519,7 @@ int launch_combine_backward(const TokenArgs& a, const char** msg) {
     }
   };
   if (wpt == 8) pick(std::integral_constant<int, 8>{});
-  else if (wpt == 4) pick(std::integral_constant<int, 4>{});
-  else if (wpt == 2) pick(std::integral_constant<int, 2>{});
-  else pick(std::integral_constant<int, 1>{});
+  else pick(std::integral_constant<int, 2>{});
   return last_error(msg);
 }
 

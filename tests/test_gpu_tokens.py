@@ -189,7 +189,7 @@ def test_far_rows():
 
 
 # ---------------------------------------------------------------- combine and its gradient
-@pytest.mark.parametrize("T,N,k,E", CASES + [(3000, 264, 3, 9)])
+@pytest.mark.parametrize("T,N,k,E", CASES + [(3000, 264, 3, 9), (2500, 648, 2, 5), (2600, 1808, 5, 9), (610, 1040, 4, 8)])
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("bad", [0.0, 0.4])
 def test_combine_and_gradient(T, N, k, E, weighted, bad):
