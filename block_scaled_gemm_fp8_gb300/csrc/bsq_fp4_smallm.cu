@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include "bsq_decode.cuh"
+#include "bsq_internal.h"
 #include "bsq_moe_internal.h"
 #include "../../include/bsq.h"
 
@@ -122,6 +123,9 @@ __device__ __forceinline__ void group_sync(int group) {
 }
 
 constexpr int kStepK = 256;             // k of a step: 128 bytes of a row of W, a whole cache line
+constexpr int kRoutedWords = kMaxExperts / 32;
+// Dynamic shared memory a CTA can ask for: what the kernel declares itself counts against the same 227 KB.
+constexpr int kMaxSmem = 227 * 1024 - kRoutedWords * 4;
 
 // MT: 16-row groups of W a warp; RW: warps beside one another in N; KW: in k; NT: groups of 8 tokens
 // per pass over W; STAGES: steps in flight; CTAS an SM shall hold.  ALIGNED: K % 256 == 0 and
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
     // With fewer rows than experts blockIdx.y counts the experts that have any, so that few CTAs find
     // nothing to do (8 rows on 512 experts of 2816 x 2048: 10 us against 29).
     const bool sparse = gridDim.y < static_cast<unsigned>(p.E);
-    __shared__ uint32_t routed[32];       // E <= 1024
+    __shared__ uint32_t routed[kRoutedWords];
     bool bad = false;
     for (int i0 = 0; i0 < p.E; i0 += kThreads) {
       const int i = i0 + tid;
@@ -364,10 +368,10 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   constexpr int kRows = 16 * MT * RW;
   const dim3 grid(static_cast<unsigned>((a.N + kRows - 1) / kRows), static_cast<unsigned>(a.offsets ? (a.S < a.E ? a.S : a.E) : 1));
   constexpr int kRing = KW * STAGES * (kRows * 128 + NT * 8 * 512), kRed = KW * 8 * (kRows + 4) * 4;
-  static_assert(kRed <= kRing && kRing <= 224 * 1024, "shared memory");
+  static_assert(kRed <= kRing && kRing <= kMaxSmem, "shared memory");
   const int64_t spitch = a.K / (FMT == BSQ_NVFP4 ? 16 : 32);
   const int64_t with = kRing + kRows * (spitch + 16);
-  const bool aligned = a.K % kStepK == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & (spitch % 16 ? 7u : 15u)) == 0 && with <= 227 * 1024;
+  const bool aligned = a.K % kStepK == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & (spitch % 16 ? 7u : 15u)) == 0 && with <= kMaxSmem;
   const int smem = aligned ? static_cast<int>(with) : kRing;
   const auto kernel = aligned ? fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, true> : fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, false>;
   cudaError_t e = cudaSuccess;
