@@ -374,8 +374,10 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   const bool aligned = a.K % kStepK == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & (spitch % 16 ? 7u : 15u)) == 0 && with <= kMaxSmem;
   const int smem = aligned ? static_cast<int>(with) : kRing;
   const auto kernel = aligned ? fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, true> : fp4_smallm_kernel<FMT, MT, RW, KW, NT, STAGES, CTAS, false>;
+  // The limit is the function's, for all host threads: always the largest, so that no call lowers it
+  // between another's setting and its launch.
   cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e == cudaSuccess) {
     kernel<<<grid, RW * KW * 32, smem, a.stream>>>(p);
     e = cudaGetLastError();
