@@ -33,6 +33,7 @@ int last_error(const char** msg) {
 
 // ---------------------------------------------------------------- sort
 constexpr int kSortWarps = 32;
+constexpr int kMaxSortSmem = (kSortWarps + 2) * kMaxExperts * 4;
 constexpr int kAheadS = 4;       // ids a lane loads before the first is counted, where it does not hold them all
 
 // Counts a warp's 32 slots: the number of slots of the same expert before each, within the warp's run;
@@ -412,11 +413,10 @@ bool sixteen_fit() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   int k = known[dev].load(std::memory_order_relaxed);
   if (k == 0) {
-    const size_t smem = static_cast<size_t>(kSortWarps + 2) * kMaxExperts * 4;
     const auto kernel = sort_experts_kernel<16>;
-    const SortLaunch l(16, smem, nullptr);
+    const SortLaunch l(16, kMaxSortSmem, nullptr);
     int clusters = 0;
-    const bool asked = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess &&
+    const bool asked = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSortSmem) == cudaSuccess &&
                        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                        cudaOccupancyMaxActiveClusters(&clusters, kernel, &l.cfg) == cudaSuccess;
     if (!asked) cudaGetLastError();
@@ -442,8 +442,10 @@ int launch_sort_experts(const SortArgs& a, const char** msg) {
   else if (run <= 256) kernel = sort_experts_kernel<8>;
   else if (run <= 512) kernel = sort_experts_kernel<16>;
   const size_t smem = static_cast<size_t>(kSortWarps + 2) * a.E * 4;
+  // The limit is the function's, for all host threads: always the largest, so that no call lowers it
+  // between another's setting and its launch.
   cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (smem > 47 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSortSmem);
   if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) {
     SortLaunch l(ctas, smem, a.stream);

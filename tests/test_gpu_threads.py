@@ -72,3 +72,19 @@ def test_products_of_two_lengths(fmt, E, rows, Ks):
     torch.cuda.synchronize()
     at_once(calls)
     assert all(torch.equal(got, want) for got, want in results)
+
+
+@pytest.mark.parametrize("T", [64, 512, 3000])
+def test_sorts_for_two_numbers_of_experts(T):
+    """One CTA, a cluster of eight and one of sixteen."""
+    calls, results, held = [], [], []
+    for i in range(THREADS):
+        E, side = (1024, 400)[i % 2], torch.cuda.Stream()
+        ids = torch.randint(0, E, (T, 8), generator=torch.Generator().manual_seed(i)).to(I32).cuda()
+        got = [torch.zeros(n, dtype=I32, device="cuda") for n in (E, 8 * T, 8 * T)]
+        held.append((ids, side))
+        results.append((got, bsq.sort_experts(ids, E)))
+        calls.append((bsq.lib().bsq_sort_experts, (ptr(ids), T, 8, E, *map(ptr, got), ctypes.c_void_p(side.cuda_stream))))
+    torch.cuda.synchronize()
+    at_once(calls)
+    assert all(torch.equal(a, b.view(-1)) for got, want in results for a, b in zip(got, want))
