@@ -33,6 +33,7 @@ bsq_status fail(bsq_status s, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
   va_end(ap);
+  if (s == BSQ_ERR_CUDA) cudaGetLastError();   // reported here: not also by the caller's next CUDA call
   return s;
 }
 
