@@ -48,7 +48,11 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
   return v;
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// By e^-|x|, which does not overflow: a small sigmoid keeps its bits as far as float32 has numbers (x = -103).
+__device__ __forceinline__ float sigmoid(float x) {
+  const float e = expf(-fabsf(x));
+  return (x >= 0.f ? 1.f : e) / (1.f + e);
+}
 // e^x for the softmax's x <= 0, as 2^(x log2 e): the rounded product adds |x| 2^-24 to the relative
 // error, as the rounding of x itself does.  expf's own splitting of x costs three times as much.
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }

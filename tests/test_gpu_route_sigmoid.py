@@ -1,0 +1,76 @@
+"""The router's sigmoid gate where it is used and where it is steep: choices by sigmoid + bias of one size, weights and gradients of
+logits far from zero, against the definition in 64 bits.
+
+Tolerance.  u = 2^-24, z = 2^-149 (the smallest float32).  With e = exp(-|l|), off by at most 2 ulp (4 u, below 2^-126 2 z), s and
+1 - s are 1 / (1 + e) and e / (1 + e): the sum and the division round once each, so both are off by at most 6 u of
+themselves and 3 z.  The score s + bias rounds once more: two scores further apart than 2 (6 u + u max |score|) keep their order.
+  weight, not renormalized: the factor's product once more, 7 u.
+  gradient factor g s (1 - s): 2 * 6 u and three products: 15 u, 16 u with the terms of second order; each of s, 1 - s and
+the products loses 3 z at most where it is that small: 8 z (|g| + 1).
+  renormalized q = s / sum: the sum of k positive terms over five exchanges 5 u + 6 u, the quotient u, s itself 6 u: 18 u of q; the
+terms' 3 z are 3 z / sum of q each, and 3 z k q / sum by the sum: dq = 3 z (1 + k q) / sum.
+  mean = sum g q: |err| <= 24 u sum |g| q + sum |g| dq (the product and five exchanges on top).
+  gradient q (g - mean) (1 - s), with m = sum |g| q: q (|g| + m) (18 + 6 + 3 + 1) u + q (24 u m + sum |g| dq) + dq (|g| + m), all
+times 1 - s; 52 u q (|g| + m) bounds the first terms; and 8 z (|g| + 1) as above.
+The output's type adds half a step: 2^-8 of a BF16 value.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_gemm_fp8_gb300 import bsq
+
+pytestmark = pytest.mark.gpu
+
+U, Z = 2.0 ** -24, 2.0 ** -149
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def both(x):
+    """(s, 1 - s) of a float64 array, each to its own last bits."""
+    e = np.exp(-np.abs(x))
+    big, small = 1 / (1 + e), e / (1 + e)
+    return np.where(x >= 0, big, small), np.where(x >= 0, small, big)
+
+
+def check(x, ids, grad, renorm, factor):
+    """The weights and the gradient of logits x [T, E] with the choice ids [T, k] against 64 bits."""
+    ids = torch.as_tensor(ids, dtype=torch.int32)
+    got = bsq.route_backward(x.cuda(), ids.cuda(), grad.cuda(), gate="sigmoid", renormalize=renorm, factor=factor)
+    got = got.cpu().double().numpy()
+    at = ids.long().numpy()
+    s, rest = both(np.take_along_axis(x.double().numpy(), at, axis=1))
+    g = float(np.float32(factor)) * grad.double().numpy()
+    k = at.shape[1]
+    if renorm:
+        total = s.sum(axis=1, keepdims=True)
+        q = s / total
+        size, mean = (abs(g) * q).sum(axis=1, keepdims=True), (g * q).sum(axis=1, keepdims=True)
+        ref = q * (g - mean) * rest
+        dq = 3 * Z * (1 + k * q) / total
+        bound = rest * (52 * U * q * (abs(g) + size) + q * (abs(g) * dq).sum(axis=1, keepdims=True) + dq * (abs(g) + size))
+    else:
+        ref = g * s * rest
+        bound = 16 * U * abs(ref)
+    bound = bound + 8 * Z * (abs(g) + 1) + (2.0 ** -8 if x.dtype == BF16 else 0) * abs(ref)
+    err = np.abs(np.take_along_axis(got, at, axis=1) - ref)
+    assert np.isfinite(got).all() and (err <= bound).all(), (err / np.maximum(bound, 1e-300)).max()
+    other = np.ones(x.shape, bool)
+    np.put_along_axis(other, at, False, axis=1)
+    assert not got[other].any()
+
+
+def distinct(T, E, k, seed):
+    return torch.rand((T, E), generator=torch.Generator().manual_seed(seed)).argsort(dim=1)[:, :k]
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("low", [-30.0, -88.0, -90.0, -95.0, -100.0])
+def test_weights_of_small_sigmoids(low, renorm):
+    """Sigmoids are those of float32 as far as it has numbers, down to a logit of -103."""
+    x = low + torch.rand((9, 12), generator=torch.Generator().manual_seed(5))
+    ids, w = (t.cpu() for t in bsq.route(x.cuda(), 3, gate="sigmoid", renormalize=renorm))
+    s = both(np.take_along_axis(x.double().numpy(), ids.long().numpy(), axis=1))[0]
+    total = s.sum(axis=1, keepdims=True) if renorm else np.ones((9, 1))
+    bound = (18 if renorm else 7) * U * s / total + 3 * Z * (1 + 3 * s / total * renorm) / total
+    assert (np.abs(w.double().numpy() - s / total) <= bound).all()
