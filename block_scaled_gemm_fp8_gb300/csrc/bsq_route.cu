@@ -6,7 +6,7 @@
 //   sigmoid   w_j = f s_j, s = sigmoid(logit), or renormalized f s_j / sum_chosen s
 //   softmax   dl_e = p_e (g_e - sum_chosen g p),           g = f grad_w at the chosen, else 0
 //             (renormalized: the same over the chosen, all other gradients zero)
-//   sigmoid   dl_j = g_j s_j (1 - s_j), renormalized (g_j - sum g s / sum s) s_j (1 - s_j) / sum s
+//   sigmoid   dl_j = g_j s_j (1 - s_j), renormalized q_j (g_j - sum g q) (1 - s_j), q = s / sum s
 //
 // A warp per token, V = E / 32 experts a lane in registers.  Scores are compared as
 // integers of the same order, so that one warp-wide integer maximum finds the best and the
@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
     const float s = have ? sigmoid(chosen) : 0.f;
     d = g * s * (1.f - s);
     if (renorm) {
-      const float sum = warp_sum(s), mass = warp_sum(g * s);
-      d = sum != 0.f ? (g - mass / sum) / sum * s * (1.f - s) : 0.f;
+      // divided first: the quotients are at most 1 however small the sum is
+      const float sum = warp_sum(s), q = sum != 0.f ? s / sum : 0.f;
+      d = q * (g - warp_sum(g * q)) * (1.f - s);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = 0.f;

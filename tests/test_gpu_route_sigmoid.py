@@ -74,3 +74,16 @@ def test_weights_of_small_sigmoids(low, renorm):
     total = s.sum(axis=1, keepdims=True) if renorm else np.ones((9, 1))
     bound = (18 if renorm else 7) * U * s / total + 3 * Z * (1 + 3 * s / total * renorm) / total
     assert (np.abs(w.double().numpy() - s / total) <= bound).all()
+
+
+@pytest.mark.parametrize("factor", [1.0, 1e3])
+@pytest.mark.parametrize("low", [-70.0, -80.0, -82.0, -86.0, -87.5, -88.6])
+def test_renormalized_gradient_of_small_sigmoids(low, factor):
+    """Sums of sigmoids down to 1e-38, large gradients: the quotients are of the size of one."""
+    T, E, k = 16, 40, 4
+    g = torch.Generator().manual_seed(int(-10 * low))
+    x = low + 0.7 * torch.rand((T, E), generator=g)
+    ids = distinct(T, E, k, 1)
+    x[torch.arange(0, T, 2), ids[::2, 1].long()] = -100.0
+    x[3, ids[3, 0]] = 2.0
+    check(x, ids, 5 * torch.randn((T, k), generator=g), True, factor)
