@@ -222,11 +222,12 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
     for (int v = 0; v < V; ++v) p[v] = full ? p[v] * share : 0.f;
   } else {
     const float s = have ? sigmoid(chosen) : 0.f;
-    d = g * s * (1.f - s);
+    const float rest = sigmoid(-chosen);       // 1 - s, whose bits that difference loses where s is near 1
+    d = g * s * rest;
     if (renorm) {
       // divided first: the quotients are at most 1 however small the sum is
       const float sum = warp_sum(s), q = sum != 0.f ? s / sum : 0.f;
-      d = q * (g - warp_sum(g * q)) * (1.f - s);
+      d = q * (g - warp_sum(g * q)) * rest;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = 0.f;

@@ -12,7 +12,7 @@ terms' 3 z are 3 z / sum of q each, and 3 z k q / sum by the sum: dq = 3 z (1 + 
   mean = sum g q: |err| <= 24 u sum |g| q + sum |g| dq (the product and five exchanges on top).
   gradient q (g - mean) (1 - s), with m = sum |g| q: q (|g| + m) (18 + 6 + 3 + 1) u + q (24 u m + sum |g| dq) + dq (|g| + m), all
 times 1 - s; 52 u q (|g| + m) bounds the first terms; and 8 z (|g| + 1) as above.
-The output's type adds half a step: 2^-8 of a BF16 value.
+The output's type adds half a step: 2^-8 of a BF16 value, and 2^-134 below 2^-126, where BF16 numbers lie 2^-133 apart.
 """
 
 import numpy as np
@@ -53,7 +53,7 @@ def check(x, ids, grad, renorm, factor):
     else:
         ref = g * s * rest
         bound = 16 * U * abs(ref)
-    bound = bound + 8 * Z * (abs(g) + 1) + (2.0 ** -8 if x.dtype == BF16 else 0) * abs(ref)
+    bound = bound + 8 * Z * (abs(g) + 1) + (np.maximum(2.0 ** -8 * abs(ref), 2.0 ** -134) if x.dtype == BF16 else 0)
     err = np.abs(np.take_along_axis(got, at, axis=1) - ref)
     assert np.isfinite(got).all() and (err <= bound).all(), (err / np.maximum(bound, 1e-300)).max()
     other = np.ones(x.shape, bool)
@@ -87,3 +87,15 @@ def test_renormalized_gradient_of_small_sigmoids(low, factor):
     x[torch.arange(0, T, 2), ids[::2, 1].long()] = -100.0
     x[3, ids[3, 0]] = 2.0
     check(x, ids, 5 * torch.randn((T, k), generator=g), True, factor)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("low,high", [(8, 12), (12, 20), (20, 60), (60, 88), (88, 104)])
+def test_gradient_of_large_logits(low, high, renorm):
+    """1 - s far below a step of s."""
+    T, E, k = 24, 33, 5
+    g = torch.Generator().manual_seed(low)
+    for dtype in (F32, BF16):
+        x = (low + (high - low) * torch.rand((T, E), generator=g)).to(dtype)
+        check(x, distinct(T, E, k, 2), torch.randn((T, k), generator=g), renorm, 2.5)
+        check(-x, distinct(T, E, k, 2), torch.randn((T, k), generator=g), renorm, 2.5)
