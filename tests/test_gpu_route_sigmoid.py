@@ -99,3 +99,29 @@ def test_gradient_of_large_logits(low, high, renorm):
         x = (low + (high - low) * torch.rand((T, E), generator=g)).to(dtype)
         check(x, distinct(T, E, k, 2), torch.randn((T, k), generator=g), renorm, 2.5)
         check(-x, distinct(T, E, k, 2), torch.randn((T, k), generator=g), renorm, 2.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,E,k", [(64, 96, 6), (40, 256, 8), (7, 12, 12), (16, 600, 4)])
+def test_choice_by_sigmoids_and_biases_of_one_size(dtype, T, E, k):
+    g = torch.Generator().manual_seed(E)
+    x = (1.5 * torch.randn((T, E), generator=g)).to(dtype)
+    bias = 0.2 * torch.randn(E, generator=g)
+    x[:, 1::4], bias[1::4] = x[:, 0::4], bias[0::4]        # pairs of equal scores
+    ids, w = (t.cpu() for t in bsq.route(x.cuda(), k, gate="sigmoid", bias=bias.cuda()))
+    s = both(x.double().numpy())[0]
+    score = s + bias.double().numpy()
+    far = 2 * (6 * U + U * np.abs(score).max())
+    assert len(set(np.argsort(-s, axis=1)[:, 0]) & set(np.argsort(-score, axis=1)[:, 0])) < T or T < 8      # the bias changes choices
+    for t in range(T):
+        row = ids[t].tolist()
+        assert len(set(row)) == k
+        mine = score[t, row]
+        assert (mine[:-1] >= mine[1:] - far).all()
+        rest = np.delete(score[t], row)
+        assert rest.size == 0 or rest.max() <= mine[-1] + far
+        for e in row:
+            if e % 4 == 1:                                  # of two equal ones the lower index comes first
+                assert row.index(e - 1) == row.index(e) - 1
+    v = np.take_along_axis(s, ids.long().numpy(), axis=1)
+    assert (np.abs(w.double().numpy() - v / v.sum(axis=1, keepdims=True)) <= 19 * U).all()
