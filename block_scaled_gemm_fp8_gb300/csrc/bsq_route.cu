@@ -48,11 +48,14 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
   return v;
 }
-// By e^-|x|, which does not overflow: a small sigmoid keeps its bits as far as float32 has numbers (x = -103).
-__device__ __forceinline__ float sigmoid(float x) {
-  const float e = expf(-fabsf(x));
-  return (x >= 0.f ? 1.f : e) / (1.f + e);
+// {s, 1 - s} of the sigmoid, by e^-|x|, which does not overflow: each keeps its bits as far as float32 has numbers
+// (|x| = 103).  One reciprocal for both (16384 x 128, the gradient of eight: 5.3 us with a
+// division each, 5.0 so).
+__device__ __forceinline__ float2 sigmoids(float x) {
+  const float e = expf(-fabsf(x)), r = 1.f / (1.f + e), er = e * r;
+  return x >= 0.f ? make_float2(r, er) : make_float2(er, r);
 }
+__device__ __forceinline__ float sigmoid(float x) { return sigmoids(x).x; }
 // e^x for the softmax's x <= 0, as 2^(x log2 e): the rounded product adds |x| 2^-24 to the relative
 // error, as the rounding of x itself does.  expf's own splitting of x costs three times as much.
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
@@ -221,8 +224,9 @@ __global__ void __launch_bounds__(kWarpsR * 32) route_backward_kernel(const T* _
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = full ? p[v] * share : 0.f;
   } else {
-    const float s = have ? sigmoid(chosen) : 0.f;
-    const float rest = sigmoid(-chosen);       // 1 - s, whose bits that difference loses where s is near 1
+    // 1 - s would lose its bits where s is near 1
+    const float2 both = sigmoids(chosen);
+    const float s = have ? both.x : 0.f, rest = both.y;
     d = g * s * rest;
     if (renorm) {
       // divided first: the quotients are at most 1 however small the sum is

@@ -2,16 +2,16 @@
 logits far from zero, against the definition in 64 bits.
 
 Tolerance.  u = 2^-24, z = 2^-149 (the smallest float32).  With e = exp(-|l|), off by at most 2 ulp (4 u, below 2^-126 2 z), s and
-1 - s are 1 / (1 + e) and e / (1 + e): the sum and the division round once each, so both are off by at most 6 u of
-themselves and 3 z.  The score s + bias rounds once more: two scores further apart than 2 (6 u + u max |score|) keep their order.
-  weight, not renormalized: the factor's product once more, 7 u.
-  gradient factor g s (1 - s): 2 * 6 u and three products: 15 u, 16 u with the terms of second order; each of s, 1 - s and
+1 - s are r = 1 / (1 + e) and e r: the sum, the reciprocal and the product round once each, so both are off by at most 7 u of
+themselves and 3 z.  The score s + bias rounds once more: two scores further apart than 2 (7 u + u max |score|) keep their order.
+  weight, not renormalized: the factor's product once more, 8 u.
+  gradient factor g s (1 - s): 2 * 7 u and three products: 17 u, 18 u with the terms of second order; each of s, 1 - s and
 the products loses 3 z at most where it is that small: 8 z (|g| + 1).
-  renormalized q = s / sum: the sum of k positive terms over five exchanges 5 u + 6 u, the quotient u, s itself 6 u: 18 u of q; the
+  renormalized q = s / sum: the sum of k positive terms over five exchanges 5 u + 7 u, the quotient u, s itself 7 u: 20 u of q; the
 terms' 3 z are 3 z / sum of q each, and 3 z k q / sum by the sum: dq = 3 z (1 + k q) / sum.
-  mean = sum g q: |err| <= 24 u sum |g| q + sum |g| dq (the product and five exchanges on top).
-  gradient q (g - mean) (1 - s), with m = sum |g| q: q (|g| + m) (18 + 6 + 3 + 1) u + q (24 u m + sum |g| dq) + dq (|g| + m), all
-times 1 - s; 52 u q (|g| + m) bounds the first terms; and 8 z (|g| + 1) as above.
+  mean = sum g q: |err| <= 26 u sum |g| q + sum |g| dq (the product and five exchanges on top).
+  gradient q (g - mean) (1 - s), with m = sum |g| q: q (|g| + m) (20 + 7 + 3 + 1) u + q (26 u m + sum |g| dq) + dq (|g| + m), all
+times 1 - s; 58 u q (|g| + m) bounds the first terms; and 8 z (|g| + 1) as above.
 The output's type adds half a step: 2^-8 of a BF16 value, and 2^-134 below 2^-126, where BF16 numbers lie 2^-133 apart.
 """
 
@@ -49,10 +49,10 @@ def check(x, ids, grad, renorm, factor):
         size, mean = (abs(g) * q).sum(axis=1, keepdims=True), (g * q).sum(axis=1, keepdims=True)
         ref = q * (g - mean) * rest
         dq = 3 * Z * (1 + k * q) / total
-        bound = rest * (52 * U * q * (abs(g) + size) + q * (abs(g) * dq).sum(axis=1, keepdims=True) + dq * (abs(g) + size))
+        bound = rest * (58 * U * q * (abs(g) + size) + q * (abs(g) * dq).sum(axis=1, keepdims=True) + dq * (abs(g) + size))
     else:
         ref = g * s * rest
-        bound = 16 * U * abs(ref)
+        bound = 18 * U * abs(ref)
     bound = bound + 8 * Z * (abs(g) + 1) + (np.maximum(2.0 ** -8 * abs(ref), 2.0 ** -134) if x.dtype == BF16 else 0)
     err = np.abs(np.take_along_axis(got, at, axis=1) - ref)
     assert np.isfinite(got).all() and (err <= bound).all(), (err / np.maximum(bound, 1e-300)).max()
@@ -72,7 +72,7 @@ def test_weights_of_small_sigmoids(low, renorm):
     ids, w = (t.cpu() for t in bsq.route(x.cuda(), 3, gate="sigmoid", renormalize=renorm))
     s = both(np.take_along_axis(x.double().numpy(), ids.long().numpy(), axis=1))[0]
     total = s.sum(axis=1, keepdims=True) if renorm else np.ones((9, 1))
-    bound = (18 if renorm else 7) * U * s / total + 3 * Z * (1 + 3 * s / total * renorm) / total
+    bound = (20 if renorm else 8) * U * s / total + 3 * Z * (1 + 3 * s / total * renorm) / total
     assert (np.abs(w.double().numpy() - s / total) <= bound).all()
 
 
@@ -111,7 +111,7 @@ def test_choice_by_sigmoids_and_biases_of_one_size(dtype, T, E, k):
     ids, w = (t.cpu() for t in bsq.route(x.cuda(), k, gate="sigmoid", bias=bias.cuda()))
     s = both(x.double().numpy())[0]
     score = s + bias.double().numpy()
-    far = 2 * (6 * U + U * np.abs(score).max())
+    far = 2 * (7 * U + U * np.abs(score).max())
     assert len(set(np.argsort(-s, axis=1)[:, 0]) & set(np.argsort(-score, axis=1)[:, 0])) < T or T < 8      # the bias changes choices
     for t in range(T):
         row = ids[t].tolist()
@@ -124,4 +124,4 @@ def test_choice_by_sigmoids_and_biases_of_one_size(dtype, T, E, k):
             if e % 4 == 1:                                  # of two equal ones the lower index comes first
                 assert row.index(e - 1) == row.index(e) - 1
     v = np.take_along_axis(s, ids.long().numpy(), axis=1)
-    assert (np.abs(w.double().numpy() - v / v.sum(axis=1, keepdims=True)) <= 19 * U).all()
+    assert (np.abs(w.double().numpy() - v / v.sum(axis=1, keepdims=True)) <= 21 * U).all()
