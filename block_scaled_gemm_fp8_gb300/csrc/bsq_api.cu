@@ -709,7 +709,7 @@ bsq_status bsq_route_backward(int32_t dtype, const void* logits, int64_t T, int6
   bsq::RouteArgs a{dtype, logits, T, static_cast<int>(E), k, gate, renormalize != 0, nullptr, factor, const_cast<int32_t*>(ids), nullptr,
                    grad_weights, grad_logits, static_cast<cudaStream_t>(stream)};
   const char* msg = "";
-  if (bsq::launch_route_backward(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
+  if (bsq::launch_route(a, &msg) != 0) return fail(BSQ_ERR_CUDA, "%s: %s", what, msg);
   return BSQ_OK;
 }
 

@@ -79,8 +79,6 @@ struct Scales<BSQ_MXFP4> {
   static constexpr int kCount = 1;
   static constexpr uint32_t kOne = 127;      // a scale of 1, for codes that are not there
   uint32_t c[1];
-  static __device__ __forceinline__ bool ordinary(float) { return false; }
-  __device__ __forceinline__ void set_ordinary(uint32_t, float) {}
   __device__ __forceinline__ bool set(uint32_t bytes, float) {
     c[0] = bytes * 0x00800080u + 126u * 0x00800080u;   // (b + 126) << 7 in both halves
     return bytes > 128u;
@@ -184,7 +182,8 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
   const uint32_t tpitch = spitch + 16;               // of the scales in shared memory: rows fall in different banks
   const uint8_t* sbase = p.ws + row0 * spitch;
   const float ts = FMT == BSQ_NVFP4 ? __ldg(p.ts + e) : 0.f;
-  const bool ordinary = Scales<FMT>::ordinary(ts);
+  bool ordinary = false;
+  if constexpr (FMT == BSQ_NVFP4) ordinary = Scales<FMT>::ordinary(ts);
   uint8_t* tile = smem + KW * STAGES * kStage;
   const uint32_t ring = smem_u32(smem) + group * (STAGES * kStage);
   const uint8_t* ring_ptr = smem + group * (STAGES * kStage);
@@ -285,10 +284,13 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
         const float tsh = ALIGNED || kStepK * step + 64 * t + 32 * h < p.K ? ts : 0.f;
         const auto scale_bytes = [&](int i) { return sv[i >> 1][i & 1] >> (8 * kCount * h) & (kCount == 2 ? 0xFFFFu : 0xFFu); };
         bool slow = false;
-        if (ordinary) {
+        if constexpr (FMT == BSQ_NVFP4) {
+          if (ordinary) {
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) f[i >> 1][i & 1].set_ordinary(scale_bytes(i), tsh);
-        } else {
+            for (int i = 0; i < 2 * MT; ++i) f[i >> 1][i & 1].set_ordinary(scale_bytes(i), tsh);
+          }
+        }
+        if (!ordinary) {
 #pragma unroll
           for (int i = 0; i < 2 * MT; ++i) slow |= f[i >> 1][i & 1].set(scale_bytes(i), tsh);
           slow = __any_sync(kFull, slow);

@@ -10,7 +10,7 @@ namespace bsq {
 
 constexpr int kMaxSlots = 32;   // slots a token (k): one lane of a warp each
 
-// bsq_route (ids, weights written) and bsq_route_backward (ids read, grad_weights, grad_logits).
+// bsq_route (ids, weights written), or with grad_logits bsq_route_backward (ids read, grad_weights).
 struct RouteArgs {
   int dtype;               // bsq_dtype of logits and grad_logits
   const void* logits;      // [T][E]
@@ -26,7 +26,6 @@ struct RouteArgs {
   cudaStream_t stream;
 };
 int launch_route(const RouteArgs& a, const char** msg);
-int launch_route_backward(const RouteArgs& a, const char** msg);
 
 struct SortArgs {
   const int32_t* ids;      // [n]

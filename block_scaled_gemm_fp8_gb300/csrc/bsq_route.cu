@@ -289,13 +289,10 @@ int launch_typed(const RouteArgs& a, const char** msg) {
   return 0;
 }
 
-int launch_any(const RouteArgs& a, const char** msg) {
-  return a.dtype == BSQ_DT_BF16 ? launch_typed<__nv_bfloat16>(a, msg) : launch_typed<float>(a, msg);
-}
-
 }  // namespace
 
-int launch_route(const RouteArgs& a, const char** msg) { return launch_any(a, msg); }
-int launch_route_backward(const RouteArgs& a, const char** msg) { return launch_any(a, msg); }
+int launch_route(const RouteArgs& a, const char** msg) {
+  return a.dtype == BSQ_DT_BF16 ? launch_typed<__nv_bfloat16>(a, msg) : launch_typed<float>(a, msg);
+}
 
 }  // namespace bsq

@@ -364,31 +364,21 @@ __global__ void __launch_bounds__(backward_warps(WPT) * 32) combine_backward_ker
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) dot[u] += __shfl_xor_sync(kFull, dot[u], d);
       }
-      if (WPT > 1) {
-        if (lane == 0) {
+      if (lane == 0) {
 #pragma unroll
-          for (int u = 0; u < G; ++u) part[warp][u] = dot[u];
-        }
-        __syncthreads();
-        if (there && warp % WPT == 0 && lane < G && j0 + lane < k) {
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < WPT; ++i) sum += part[warp + i][lane];
-          grad_weights[t * k + j0 + lane] = sum;
-        }
-        if (j0 + G < k) __syncthreads();
-      } else if (there && lane == 0) {
-#pragma unroll
-        for (int u = 0; u < G; ++u)
-          if (j0 + u < k) grad_weights[t * k + j0 + u] = dot[u];
+        for (int u = 0; u < G; ++u) part[warp][u] = dot[u];
       }
+      __syncthreads();
+      if (there && warp % WPT == 0 && lane < G && j0 + lane < k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) sum += part[warp + i][lane];
+        grad_weights[t * k + j0 + lane] = sum;
+      }
+      if (j0 + G < k) __syncthreads();
     }
   }
 }
-
-}  // namespace
-
-namespace {
 
 struct SortLaunch {
   cudaLaunchConfig_t cfg = {};
