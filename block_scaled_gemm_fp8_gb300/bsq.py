@@ -442,7 +442,7 @@ def route(logits, k, gate="softmax", renormalize=True, bias=None, factor=1.0, id
     float32 [T, E]) by falling score, ties to the lowest index, and their weights: factor times the softmax
     over the chosen logits (renormalize=False: over all), or the sigmoids, divided by their sum
     (renormalize=False: as they are).  bias (float32 [E]) is added to the logit (sigmoid gate: to its sigmoid) for the
-    choice alone.  A slot that no expert can fill, because logits are minus infinity or NaN, gets id -1 and weight 0."""
+    choice alone; one that is meant for the softmax's probabilities is not taken.  A slot that no expert can fill, because logits are minus infinity or NaN, gets id -1 and weight 0."""
     # one expression for the common case, here and below; what is wrong is looked for only when it fails
     if not (logits is not None and logits.dtype in _DTYPES and logits.get_device() == _current_device() and logits.is_contiguous()
             and len(logits.shape) == 2 and (bias is None or bias.dtype is torch.float32 and bias.get_device() == logits.get_device()

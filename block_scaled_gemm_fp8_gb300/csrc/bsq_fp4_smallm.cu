@@ -1,8 +1,9 @@
 // bsq_fp4_smallm.cu -- products of a few BF16 token rows with 4-bit weights (decode), dense and
 // per expert:  y[m, n] = sum_k x[m, k] deq(W)[n, k],  deq = RNE_bf16(code * RNE_bf16(scale)).
 //
-// Bound by the instructions that decode W: about 93 for 1024 MXFP4 codes of a warp, 36 of them masks on
-// a pipe that takes one every other cycle.  A CTA owns some rows of W (columns of y) and the
+// No unit is at its limit: with one or two rows an expert issue is at 0.64, the pipe of masks, permutes and shifts
+// at 0.60, HBM at 0.48 of its peak.  Most of the instructions decode W: 99 in all for 1024 MXFP4 codes
+// of a warp with 8 tokens, 126 for NVFP4 with 16.  A CTA owns some rows of W (columns of y) and the
 // whole contraction; RW warps beside one another in N and KW in k, whose groups take steps of
 // 256 k in turn, each with a ring of steps in shared memory that asynchronous copies fill.  256 k
 // are 128 bytes of a row: copies of whole cache lines, for which the load unit pays by the line
@@ -17,9 +18,10 @@
 // us against 19 at the time).  The groups' accumulators are added in their order through
 // shared memory, so results do not depend on timing.
 //
-// Measured (a graph of calls on rotated weights beyond L2): 4096 x 4096 MXFP4, one row 5.6 us; 14336 x 5120 NVFP4,
-// 1 / 8 / 16 / 32 / 64 rows 14.9 / 15.1 / 17.7 / 24.4 / 42 us (MXFP4 13.2 / 13.6 / 16.1 / 22.3 / 39.8); 64 rows
-// by 128 MXFP4 experts of 2048 x 7168 81 us, 3.8 TB/s; 512 by 64 NVFP4 experts of 2816 x 2048 80 us.
+// Measured (a graph of calls on rotated weights beyond L2): 4096 x 4096 MXFP4, one row 5.8 us; 14336 x 5120 NVFP4,
+// 1 / 8 / 16 / 32 / 64 rows 13.8 / 13.9 / 17.0 / 22.3 / 39.6 us (MXFP4 12.9 / 13.4 / 15.5 / 21.5 / 38.3); 64 rows
+// by 128 MXFP4 experts of 2048 x 7168 82.5 us, 3.7 TB/s; 509 by 64 NVFP4 experts of 2816 x 2048 76.6 us; 64 by 128
+// MXFP4 experts of 2880 x 2880, whose scales do not come in whole copies, 58.7 us (2816 x 2816: 54.9, 2 % less a byte).
 // Of those 14336 x 5120 a warp spends its time so: 1.7 us to the first copies' end of asking, 1.5
 // until the first step is there, then the instructions.
 #include <cuda_bf16.h>
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(RW * KW * 32, CTAS) fp4_smallm_kernel(const Fp
     r0 = e > 0 ? __ldg(p.offsets + e - 1) : 0;
     r1 = __ldg(p.offsets + e);
     // With fewer rows than experts blockIdx.y counts the experts that have any, so that few CTAs find
-    // nothing to do (8 rows on 512 experts of 2816 x 2048: 10 us against 29).
+    // nothing to do (8 rows on 512 experts of 2816 x 2048: 11 us against 29).
     const bool sparse = gridDim.y < static_cast<unsigned>(p.E);
     __shared__ uint32_t routed[kRoutedWords];
     bool bad = false;
@@ -393,14 +395,17 @@ int launch_typed(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
 
 // The tile and the tokens of a pass by the number of rows; every limit with both sides measured, in
 // us.  Per expert the limits are on the average, since the counts are the device's:
-//   64 experts of 2816 x 2048 NVFP4   320 rows 63.6 with 8 tokens a pass, 69.2 with 16; 384: 70.4, 71.1; 512: 84.6, 79.7 (64-row
-//                                     tiles; 48-row 82.6); 1024: 103 in 48-row tiles, 105 in 64-row ones, 126
-//                                     with 32 tokens; 2048: 170 with 16, 161 with 32
-//   32 experts of 2048 x 7168 MXFP4   160 rows 77 with 8 tokens, 86 with 16; 384: 109 in 64-row tiles, 104 in 48-row
-//   (128 experts of 1024 x 2048 would take 16 from 4 rows an expert: MXFP4 640 rows 67 with 8, 59 with 16)
-// Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 8.6 with 32
-// tokens a pass, 10.3 with 16; then 14336 x 5120 NVFP4, 8 rows 15.1 in 32-row tiles, 17.1 in
-// 96-row ones; 13 rows 21.9 in 32-row tiles, 17.5 in 96-row ones; 32 rows 24.4 in 48-row tiles, 30.2 in 96-row ones.
+//   (rows on experts of falling popularity, r^-0.7; tokens a pass are 8, 16 or 32, 16 in tiles of 64 or 48 rows of W)
+//   64 experts of 2816 x 2048 NVFP4   320 rows 68.3 with 8, 67.5 and 69.7 with 16; 384: 75.0, 69.3 and 72.1; 512: 87.8, 76.4 and
+//                                     78.6; 1024: 101.7 and 98.2 with 16, 118 with 32; 2048: 173 and 162 with 16, 152 with 32
+//   32 experts of 2048 x 7168 MXFP4   160 rows 78.4 with 8, 85.2 and 78.3 with 16; 384: 129, 105 and 99.5
+//   128 experts of 2880 x 2880 MXFP4  64 rows 58.7 with 8, 61.6 and 63.8 with 16; 640: 201, 193 and 195
+//   (128 experts of 1024 x 2048 would take 16 from 4 rows an expert: MXFP4 640 rows 66.9 with 8, 58.4 and 57.6 with 16)
+// Dense, tiles of 32 rows while that gives an SM one at most: 4096 x 4096 MXFP4, 32 rows 8.8 with 32
+// tokens a pass, 10.2 with 16; then 14336 x 5120 NVFP4, 8 rows 13.9 in 32-row tiles, 14.6 in
+// 96-row ones; 13 rows 22.2 in 32-row tiles, 17.1 in 96-row ones; 32 rows 22.2 in 48-row tiles, 24.4 in 96-row ones.
+// Of the registers 24 bytes a thread go to local memory in the 64-row tiles (16 MXFP4 and 32 NVFP4 where the scales stay in
+// global memory), 24 MXFP4 and 20 NVFP4 in the 96-row ones, up to 24 in NVFP4's 48-row ones.
 template <int FMT>
 int launch_fmt(const Fp4SmallParams& p, const Fp4Args& a, const char** msg) {
   if (a.offsets) {

@@ -12,8 +12,13 @@
 // integers of the same order, so that one warp-wide integer maximum finds the best and the
 // first lane that has it the lowest index; a chosen expert's key leaves, and the key of an expert
 // that cannot be chosen (a NaN or minus infinity) is zero.  All sums are float32.  Bound by the
-// instructions of the rounds, 0.75 of the issue slots: 16384 tokens on 128 experts, eight each, softmax over
-// all, float32: 8.3 us, the gradient 6.4 (HBM's part 1.4 and 2.6); 16 tokens on 64 experts, four each: 2.0 us.
+// instructions of the rounds, 0.75 of the issue slots (HBM's part is 1.4 us, of the gradient 2.6):
+//   float32 logits, eight experts a token, us           16384 x 128   gradient   16384 x 256   gradient
+//   softmax over all, without and with a bias             7.9   8.3        6.9    12.5  14.6        9.0
+//   softmax over the chosen                               7.3   7.6        5.7    11.1  13.3        6.7
+//   sigmoid, not renormalized                             6.9   9.0        5.0    11.1  16.1        6.1
+//   sigmoid, renormalized                                 7.7   9.9        6.2    11.8  17.0        7.0
+// 16 tokens on 64 experts, four each: 2.0 us.
 #include <cuda_bf16.h>
 
 #include "bsq_lanes.cuh"
@@ -56,8 +61,9 @@ __device__ __forceinline__ float2 sigmoids(float x) {
   return x >= 0.f ? make_float2(r, er) : make_float2(er, r);
 }
 __device__ __forceinline__ float sigmoid(float x) { return sigmoids(x).x; }
-// e^x for the softmax's x <= 0, as 2^(x log2 e): the rounded product adds |x| 2^-24 to the relative
-// error, as the rounding of x itself does.  expf's own splitting of x costs three times as much.
+// e^x for the softmax's x <= 0, as 2^(x log2 e).  The product's rounding and the constant's (0.23 2^-24 of it) add up to
+// 1.23 |x| 2^-24 to the relative error: beside the rounding of x = l - m, |x| 2^-24, or alone where that
+// difference is exact.  It is below 2^-19 for what counts, |x| <= 25 (with expf 16384 x 128 take 8.1 us, so 7.7).
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
 
 // A lane's experts by falling score, equal ones by rising index: neighbours are exchanged in turn, and

@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kThreadsT) combine_kernel(const __nv_bfloat16*
   }
 }
 
-// Small CTAs, whose warps end at about the same time (4096 tokens of four rows of 2816, four warps a token: 41.8 us
-// in CTAs of eight warps, 40.4 in CTAs of four; the weights' gradient alone 23.4 and 21.4).
+// Small CTAs, whose warps end at about the same time (4096 tokens of four rows of 2816, two warps a token: 42.5 us
+// in CTAs of eight warps, 41.1 in CTAs of four; the weights' gradient alone 22.1 and 20.2).
 constexpr int backward_warps(int wpt) { return wpt > kThreadsT / 32 ? wpt : kThreadsT / 32; }
 
 // WPT warps of a CTA share a token: 2 with tokens enough to fill the GPU, else 8.
@@ -487,8 +487,8 @@ int launch_combine(const TokenArgs& a, const char** msg) {
 
 int launch_combine_backward(const TokenArgs& a, const char** msg) {
   const int cols = static_cast<int>(a.cols), nb = static_cast<int>((a.cols + 127) / 128);
-  // four rows of 2816: 450 tokens 5.2 us with eight warps a token, 6.5 with two; 700: 7.3 and 7.1; 4096: 45 and 40.9
-  // (with one 44.1, with four 42.3)
+  // four rows of 2816: 450 tokens 5.0 us with eight warps a token, 6.2 with two; 700: 7.5 and 7.2; 4096: 44.7 and 41.1
+  // (with four 41.7; with one 44.1)
   const int wpt = a.T >= 4ll * a.num_sms ? 2 : 8;
   const int warps = backward_warps(wpt);
   const int64_t grid = (a.T * wpt + warps - 1) / warps;

@@ -370,11 +370,14 @@ typedef enum {
  * bsq_route -- the router of a mixture layer: every token's k experts of the highest score and
  * their weights.
  *   score    without a bias the logit; with one logit + bias (softmax) or sigmoid(logit) + bias
- *            (sigmoid), in float32.  The bias takes part in the choice alone.
+ *            (sigmoid), in float32.  The bias takes part in the choice alone.  Under the softmax gate
+ *            it is added before the exponentials: a bias that is meant for the probabilities
+ *            (p + bias) chooses other experts, and is not taken here.
  *   ids      int32[T][k], by falling score, ties to the lowest index
  *   weights  f32[T][k]: factor * softmax(logits)[id], or factor * sigmoid(logit[id]);
  *            renormalize != 0: factor times the softmax over the chosen logits alone, or the
- *            sigmoids divided by their sum over the chosen (zeros if that sum is zero)
+ *            sigmoids divided by their sum over the chosen (zeros if that sum is zero in float32:
+ *            logits below about -103)
  * An expert whose logit or score is a NaN or minus infinity is not chosen; slots that are left over (a
  * token whose logits are all masked) get id -1 and weight 0.  A NaN among a token's logits
  * makes its weights NaN.
@@ -389,6 +392,8 @@ bsq_status bsq_route(int32_t dtype, const void* logits, int64_t T, int64_t E, in
  *            (renormalize: over the chosen alone, zero elsewhere)
  *   sigmoid  g s (1 - s), renormalize: (g - sum g s / sum s) s (1 - s) / sum s; zero elsewhere
  * ids: bsq_route's, or any: ids outside 0..E-1 give nothing, an id given twice counts twice.
+ * A NaN among the logits makes the row's gradients NaN under the softmax over all; with
+ * renormalize and under the sigmoid gate only those of chosen NaN logits do, for no others are read.
  * The choice itself has no gradient, and so neither has the bias.
  */
 bsq_status bsq_route_backward(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate,
@@ -447,7 +452,7 @@ bsq_status bsq_combine_backward(const void* grad_out, const void* y, int64_t S, 
  * rounded once: for decoding.  Up to 64 rows stream W through a kernel of their own; more take
  * bsq_linear_forward's.  y: bf16[M][N], fully written; K == 0 gives zeros.  K <= 2^24.
  * Scales: any alignment for MXFP4, 2 bytes for NVFP4 (an expert's slice of a stacked W will do),
- * and faster where K % 256 == 0 and they are 16-byte aligned; beyond 64 rows 16 bytes.
+ * and 2 to 3 % faster where K % 256 == 0 and they are 16-byte aligned; beyond 64 rows 16 bytes.
  */
 bsq_status bsq_fp4_forward(const void* x, int64_t M, int32_t w_fmt, const void* w_data, const void* w_scale,
                            const float* w_tensor_scale, int64_t N, int64_t K, void* y, void* stream);
