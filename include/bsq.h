@@ -392,8 +392,9 @@ bsq_status bsq_route(int32_t dtype, const void* logits, int64_t T, int64_t E, in
  *            (renormalize: over the chosen alone, zero elsewhere)
  *   sigmoid  g s (1 - s), renormalize: (g - sum g s / sum s) s (1 - s) / sum s; zero elsewhere
  * ids: bsq_route's, or any: ids outside 0..E-1 give nothing, an id given twice counts twice.
- * A NaN among the logits makes the row's gradients NaN under the softmax over all; with
- * renormalize and under the sigmoid gate only those of chosen NaN logits do, for no others are read.
+ * A NaN among the logits makes the token's gradients NaN under the softmax over all.  With
+ * renormalize, and under the sigmoid gate, the chosen logits alone are read: a NaN among them makes
+ * the gradients of the chosen NaN, or without renormalize its own.
  * The choice itself has no gradient, and so neither has the bias.
  */
 bsq_status bsq_route_backward(int32_t dtype, const void* logits, int64_t T, int64_t E, int32_t k, int32_t gate,
